@@ -39,29 +39,29 @@ def _linear_case(name, M, N, K, dtype, bias):
 def listed():
     return [
         # the conditioning token of a 40-head layer: latency alone counts
-        _norm_case("norm, one token", False, 1, 5120, 1, True, "bf16", "bf16", "layer", "none", False, True, 1.0),
+        _norm_case("norm one token", False, 1, 5120, 1, True, "bf16", "bf16", "layer", "none", False, True, 1.0),
         # the residual between attention and MLP of a 40-head layer, modulated per latent frame
-        _norm_case("norm, 75600 tokens", False, 75600, 5120, 21, True, "bf16", "bf16", "layer", "none", False, True, 1.0),
+        _norm_case("norm 75600 tokens", False, 75600, 5120, 21, True, "bf16", "bf16", "layer", "none", False, True, 1.0),
         # a packed batch of seven clips of unequal length, norms on both sides of the block, float32
-        _norm_case("norm, ragged clips", False, 4999, 2048, 7, False, "f32", "f32", "rms", "rms", True, True, 0.5),
+        _norm_case("norm ragged clips", False, 4999, 2048, 7, False, "f32", "f32", "rms", "rms", True, True, 0.5),
         # fine-tuning step of a 16-head layer on a 32x32x32 grid
-        _norm_case("norm backward, 32768 tokens", True, 32768, 2048, 32, True, "bf16", "bf16", "layer", "none", False, True, 1.0),
+        _norm_case("norm backward 32768 tokens", True, 32768, 2048, 32, True, "bf16", "bf16", "layer", "none", False, True, 1.0),
         # one latent frame of 32 x 32 tokens (a frame-by-frame generator)
-        _rope_case("rope, one frame", False, 1, 1024, 8, 128, 1, 32, 32, 44, 42, 42, False, "head", "bf16", False),
+        _rope_case("rope one frame", False, 1, 1024, 8, 128, 1, 32, 32, 44, 42, 42, False, "head", "bf16", False),
         # two packed samples with given positions, text behind the frames, float32, half-split pairs
-        _rope_case("rope, given positions", False, 2, 4097, 4, 64, 16, 16, 16, 16, 24, 24, True, "none", "f32", True),
+        _rope_case("rope given positions", False, 2, 4097, 4, 64, 16, 16, 16, 16, 24, 24, True, "none", "f32", True),
         # Q, K, V of a 40-head layer at 21 x 45 x 80 tokens, norm over the whole token
-        _rope_case("rope, 75600 tokens", False, 1, 75600, 40, 128, 21, 45, 80, 44, 42, 42, False, "token", "bf16", False),
+        _rope_case("rope 75600 tokens", False, 1, 75600, 40, 128, 21, 45, 80, 44, 42, 42, False, "token", "bf16", False),
         # fine-tuning step of a 16-head layer on a 32x32x32 grid
-        _rope_case("rope backward, 32768 tokens", True, 1, 32768, 16, 128, 32, 32, 32, 44, 42, 42, False, "token", "bf16", False),
+        _rope_case("rope backward 32768 tokens", True, 1, 32768, 16, 128, 32, 32, 32, 44, 42, 42, False, "token", "bf16", False),
         # the attention's head-major output of a 16-head layer, on its way into the output projection
-        _quant_case("quantise, attention output", 32768, 2048, 128, "bf16"),
+        _quant_case("quantise attention output", 32768, 2048, 128, "bf16"),
         # a short ragged prompt in float32
-        _quant_case("quantise, prompt", 333, 1056, 0, "f32"),
+        _quant_case("quantise prompt", 333, 1056, 0, "f32"),
         # the modulation projection: one time embedding to six vectors of 5120
-        _linear_case("linear, one token", 1, 30720, 5120, "bf16", True),
+        _linear_case("linear one token", 1, 30720, 5120, "bf16", True),
         # the QKV projection of a 40-head layer
-        _linear_case("linear, 75600 tokens", 75600, 15360, 5120, "bf16", True),
+        _linear_case("linear 75600 tokens", 75600, 15360, 5120, "bf16", True),
     ]
 
 

@@ -75,6 +75,27 @@ cudaError_t attn_run(const void* Qp, const void* Kp, const void* Vp, const int32
                      int H, int Nq, int Nk, int d, int Cq, int Ck, float scale, void* O,
                      void* ws, cudaStream_t st);
 
+// ---- gated residual and norms (block_norm.cu)
+struct BlockNorm {
+  const svgear_norm_params* p;
+  const void *x, *y, *dr, *dh;
+  const float *gate, *scale, *shift, *weight, *bias, *post_weight;
+  const int32_t* offsets;
+  void *r, *h, *dx, *dy;
+  float *dgate, *dscale, *dshift, *dweight, *dbias, *dpost_weight;
+};
+cudaError_t block_norm_run(const BlockNorm& b, cudaStream_t st);
+size_t block_norm_back_ws_bytes(const svgear_norm_params* p);
+cudaError_t block_norm_back_run(const BlockNorm& b, void* ws, cudaStream_t st);
+
+// ---- norm, rotary positions and head order of Q, K, V (qkv_rope.cu)
+cudaError_t qkv_rope_run(const void* const in[3], const float* wq, const float* wk, const int32_t* pos,
+                         const svgear_rope_params* p, void* const out[3], cudaStream_t st);
+size_t qkv_rope_back_ws_bytes(const svgear_rope_params* p);
+cudaError_t qkv_rope_back_run(const void* const grad[3], const void* const in[2], const float* wq, const float* wk,
+                              const int32_t* pos, const svgear_rope_params* p, void* const out[3], float* dwq, float* dwk,
+                              void* ws, cudaStream_t st);
+
 // ---- TMA tensor maps (tma_host.cu)
 constexpr int kTmaMapBytes = 128;
 bool tma_available();

@@ -30,6 +30,14 @@ SVGEAR_ROUTE_MASS = 1
 SVGEAR_ROUTE_ERROR_NOV = 2
 SVGEAR_BUDGET_ROW = 0
 SVGEAR_BUDGET_GLOBAL = 1
+SVGEAR_NORM_NONE = 0
+SVGEAR_NORM_RMS = 1
+SVGEAR_NORM_LAYER = 2
+SVGEAR_PAIR_ADJACENT = 0
+SVGEAR_PAIR_HALF = 1
+SVGEAR_QKNORM_NONE = 0
+SVGEAR_QKNORM_HEAD = 1
+SVGEAR_QKNORM_TOKEN = 2
 
 
 class SvgearError(RuntimeError):
@@ -65,10 +73,27 @@ class svgear_views(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in _VIEW_FIELDS]
 
 
+class svgear_norm_params(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("D", ctypes.c_int), ("G", ctypes.c_int), ("pre", ctypes.c_int),
+                ("post", ctypes.c_int), ("eps", ctypes.c_float), ("res_scale", ctypes.c_float),
+                ("dtype", ctypes.c_int), ("res_dtype", ctypes.c_int)]
+
+
+class svgear_rope_params(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("H", ctypes.c_int), ("d", ctypes.c_int),
+                ("axes", ctypes.c_int * 3), ("grid", ctypes.c_int * 3), ("origin", ctypes.c_int * 3),
+                ("theta", ctypes.c_float * 3), ("pos_scale", ctypes.c_float * 3), ("pairing", ctypes.c_int),
+                ("norm", ctypes.c_int), ("eps", ctypes.c_float), ("dtype", ctypes.c_int),
+                ("pos_per_batch", ctypes.c_int), ("out_tokens", ctypes.c_int), ("ld", ctypes.c_int64 * 3),
+                ("batch", ctypes.c_int64 * 3), ("grad_ld", ctypes.c_int64), ("grad_batch", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _PP = ctypes.POINTER(svgear_params)
+_NP = ctypes.POINTER(svgear_norm_params)
+_RP = ctypes.POINTER(svgear_rope_params)
 
 _SIGS = {
     "svgear_version": (ctypes.c_char_p, []),
@@ -90,6 +115,12 @@ _SIGS = {
     "svgear_workspace_size": (_SZ, [_PP]),
     "svgear_forward_views": (_I, [_PP, _P, _SZ, ctypes.POINTER(svgear_views)]),
     "svgear_forward": (_I, [_P, _P, _P, _PP, _P, _P, _P, _P, _SZ, _P, ctypes.POINTER(svgear_stats)]),
+    "svgear_block_norm": (_I, [_P] * 9 + [_NP, _P, _P, _P]),
+    "svgear_block_norm_backward_workspace_size": (_SZ, [_NP]),
+    "svgear_block_norm_backward": (_I, [_P] * 10 + [_NP] + [_P] * 9 + [_SZ, _P]),
+    "svgear_qkv_rope": (_I, [_P] * 6 + [_RP] + [_P] * 4),
+    "svgear_qkv_rope_backward_workspace_size": (_SZ, [_RP]),
+    "svgear_qkv_rope_backward": (_I, [_P] * 8 + [_RP] + [_P] * 6 + [_SZ, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -129,6 +160,15 @@ def _ptr(x) -> Optional[int]:
             raise ValueError("contiguous tensor expected")
         return x.data_ptr()
     raise TypeError(f"cannot pass {type(x)} as a pointer")
+
+
+def _rows_ptr(x) -> Optional[int]:
+    """Pointer of a tensor whose strides travel in the parameter block."""
+    if x is None or isinstance(x, int):
+        return x
+    if not x.is_cuda:
+        raise ValueError("device tensor expected")
+    return x.data_ptr()
 
 
 def _stream(s) -> Optional[int]:
@@ -254,6 +294,43 @@ def svgear_forward(Q, K, V, p, init_q, init_k, O, ws, ws_bytes, stream=None, sta
         _ptr(ws), ws_bytes, _stream(stream), ctypes.byref(stats) if stats is not None else None))
 
 
+def svgear_block_norm(x, y, gate, scale, shift, weight, bias, post_weight, offsets, p, r, h, stream=None):
+    _check("svgear_block_norm", lib().svgear_block_norm(
+        _ptr(x), _ptr(y), _ptr(gate), _ptr(scale), _ptr(shift), _ptr(weight), _ptr(bias), _ptr(post_weight),
+        _ptr(offsets), ctypes.byref(p), _ptr(r), _ptr(h), _stream(stream)))
+
+
+def svgear_block_norm_backward_workspace_size(p: svgear_norm_params) -> int:
+    return lib().svgear_block_norm_backward_workspace_size(ctypes.byref(p))
+
+
+def svgear_block_norm_backward(x, y, dr, dh, gate, scale, weight, bias, post_weight, offsets, p, dx, dy, dgate,
+                               dscale, dshift, dweight, dbias, dpost_weight, ws, ws_bytes, stream=None):
+    _check("svgear_block_norm_backward", lib().svgear_block_norm_backward(
+        _ptr(x), _ptr(y), _ptr(dr), _ptr(dh), _ptr(gate), _ptr(scale), _ptr(weight), _ptr(bias),
+        _ptr(post_weight), _ptr(offsets), ctypes.byref(p), _ptr(dx), _ptr(dy), _ptr(dgate), _ptr(dscale),
+        _ptr(dshift), _ptr(dweight), _ptr(dbias), _ptr(dpost_weight), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def svgear_qkv_rope(q, k, v, wq, wk, positions, p, Q, K, V, stream=None):
+    """q, k, v may be strided rows (p.ld, p.batch); the outputs may be head-major views (p.out_tokens)."""
+    _check("svgear_qkv_rope", lib().svgear_qkv_rope(
+        _rows_ptr(q), _rows_ptr(k), _rows_ptr(v), _ptr(wq), _ptr(wk), _ptr(positions), ctypes.byref(p),
+        _rows_ptr(Q), _rows_ptr(K), _rows_ptr(V), _stream(stream)))
+
+
+def svgear_qkv_rope_backward_workspace_size(p: svgear_rope_params) -> int:
+    return lib().svgear_qkv_rope_backward_workspace_size(ctypes.byref(p))
+
+
+def svgear_qkv_rope_backward(dQ, dK, dV, q, k, wq, wk, positions, p, dq, dk, dv, dwq, dwk, ws, ws_bytes,
+                             stream=None):
+    _check("svgear_qkv_rope_backward", lib().svgear_qkv_rope_backward(
+        _rows_ptr(dQ), _rows_ptr(dK), _rows_ptr(dV), _rows_ptr(q), _rows_ptr(k), _ptr(wq), _ptr(wk),
+        _ptr(positions), ctypes.byref(p), _rows_ptr(dq), _rows_ptr(dk), _rows_ptr(dv), _ptr(dwq), _ptr(dwk),
+        _ptr(ws), ws_bytes, _stream(stream)))
+
+
 # ------------------------------------------------------- torch conveniences
 
 def dtype_code(t) -> int:
@@ -320,3 +397,244 @@ def forward(Q, K, V, Cq: int, Ck: int, iters: int, rho: float, scale: float = 0.
     st = svgear_stats() if stats else None
     svgear_forward(Q, K, V, p, init_q, init_k, O, ws, ws.numel(), stream, st)
     return O, ws, p, (st.as_dict() if st is not None else None)
+
+
+# ---- around the attention: norms, rotary positions, 4-bit projections
+#
+# These helpers run on the device their tensors are on, whatever device is
+# current, and on `stream` (default: that device's current stream).  Outputs
+# and workspaces are allocated on the same stream, so the caching allocator
+# never hands their memory to work the kernels are not ordered with.
+
+class _On:
+    """Makes `device` current, and `stream` its current stream when one is given."""
+    __slots__ = ("ctx",)
+
+    def __init__(self, device, stream):
+        import torch
+        self.ctx = []
+        if device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+            self.ctx.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+
+    def __exit__(self, *e):
+        for c in reversed(self.ctx):
+            c.__exit__(*e)
+
+
+def _want(name, t, dtype, shape, device, contiguous=True):
+    """Checks one optional tensor argument against what the call expects."""
+    if t is None:
+        return
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name}: a tensor on {device} expected, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous tensor expected")
+
+
+def _norm_call(x, y, dtype, gate, scale, shift, weight, bias, post_weight, pre, post, eps, res_scale, offsets):
+    """Checks the inputs shared by forward and backward; returns the parameter block."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError(f"x: [N, D] expected, got shape {tuple(x.shape)}")
+    N, D = x.shape
+    if not x.is_cuda:
+        raise ValueError("x: device tensor expected")
+    if not x.is_contiguous():
+        raise ValueError("x: contiguous tensor expected")
+    dev, f32 = x.device, torch.float32
+    _want("y", y, dtype, (N, D), dev)
+    G = 1
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.shape[0] < 2:
+            raise ValueError("offsets: [G + 1] int32 expected")
+        G = offsets.shape[0] - 1
+    else:
+        for t in (gate, scale, shift):
+            if t is not None:
+                G = t.shape[0]
+                break
+    _want("offsets", offsets, torch.int32, (G + 1,), dev)
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+        _want(name, t, f32, (G, D), dev)
+    for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight)):
+        _want(name, t, f32, (D,), dev)
+    codes = {torch.bfloat16: SVGEAR_BF16, torch.float32: SVGEAR_F32}
+    if x.dtype not in codes or dtype not in codes:
+        raise ValueError(f"unsupported dtype {x.dtype if x.dtype not in codes else dtype}")
+    return svgear_norm_params(N, D, G, pre, post, eps, res_scale, codes[dtype], codes[x.dtype])
+
+
+def block_norm(x, y=None, *, gate=None, scale=None, shift=None, weight=None, bias=None, post_weight=None,
+               pre: int = SVGEAR_NORM_LAYER, post: int = SVGEAR_NORM_NONE, eps: float = 1e-6,
+               res_scale: float = 1.0, offsets=None, dtype=None, want_h: bool = True, stream=None):
+    """r = res_scale x + gate P(y) post_weight and h = (Q(r) weight + bias)(1 + scale) + shift through
+    svgear_block_norm.  x [N, D], y [N, D] or None (r is x); gate, scale, shift [G, D] with the groups given
+    by offsets [G+1] or N/G rows each.  h has y's type, or `dtype` (default x's) without y.
+    Returns (r, h); h is None with want_h=False."""
+    import torch
+    if y is not None and dtype is not None and dtype != y.dtype:
+        raise ValueError(f"dtype {dtype} differs from y's {y.dtype}")
+    dtype = y.dtype if y is not None else dtype or x.dtype
+    p = _norm_call(x, y, dtype, gate, scale, shift, weight, bias, post_weight, pre, post, eps, res_scale, offsets)
+    with _On(x.device, stream):
+        r = torch.empty_like(x) if y is not None else None
+        h = torch.empty_like(x, dtype=dtype) if want_h else None
+        svgear_block_norm(x, y, gate, scale, shift, weight, bias, post_weight, offsets, p, r, h)
+    return (x if r is None else r), h
+
+
+def block_norm_backward(x, y, dr, dh, *, gate=None, scale=None, shift=None, weight=None, bias=None,
+                        post_weight=None, pre: int = SVGEAR_NORM_LAYER, post: int = SVGEAR_NORM_NONE,
+                        eps: float = 1e-6, res_scale: float = 1.0, offsets=None, stream=None):
+    """Gradients of block_norm for the gradients dr of r and dh of h (one may be None), through
+    svgear_block_norm_backward.  The other arguments are the forward's.  Returns a dict with dx, dy, dgate,
+    dscale, dshift, dweight, dbias and dpost_weight; None for what the forward was not given."""
+    import torch
+    if dr is None and dh is None:
+        raise ValueError("dr or dh expected")
+    dtype = y.dtype if y is not None else dh.dtype if dh is not None else x.dtype
+    p = _norm_call(x, y, dtype, gate, scale, shift, weight, bias, post_weight, pre, post, eps, res_scale, offsets)
+    _want("dr", dr, x.dtype, x.shape, x.device)
+    _want("dh", dh, dtype, x.shape, x.device)
+    like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
+    with _On(x.device, stream):
+        out = {"dx": torch.empty_like(x), "dy": like(y), "dgate": like(gate), "dscale": like(scale),
+               "dshift": like(shift), "dweight": like(weight), "dbias": like(bias),
+               "dpost_weight": like(post_weight)}
+        ws = workspace(svgear_block_norm_backward_workspace_size(p), x.device)
+        svgear_block_norm_backward(x, y, dr, dh, gate, scale, weight, bias, post_weight, offsets, p, out["dx"],
+                                   out["dy"], out["dgate"], out["dscale"], out["dshift"], out["dweight"],
+                                   out["dbias"], out["dpost_weight"], ws, ws.numel())
+    return out
+
+
+def _three(v, kind):
+    return tuple(kind(x) for x in v) if isinstance(v, (tuple, list)) else (kind(v),) * 3
+
+
+def rope_params(B, N, H, d, axes, grid=(0, 0, 0), origin=0, theta=10000.0, pos_scale=1.0,
+                pairing: int = SVGEAR_PAIR_ADJACENT, norm: int = SVGEAR_QKNORM_NONE, eps: float = 1e-6,
+                dtype: int = SVGEAR_BF16, pos_per_batch: int = 0, out_tokens: int = 0) -> svgear_rope_params:
+    """Parameter block for dense rows [B, N, H, d]; origin, theta and pos_scale are one value or one per axis."""
+    if len(axes) != 3 or len(grid) != 3:
+        raise ValueError("axes and grid have three entries: time, height, width")
+    I3, F3, L3 = ctypes.c_int * 3, ctypes.c_float * 3, ctypes.c_int64 * 3
+    ld, batch = H * d, N * H * d
+    return svgear_rope_params(B, N, H, d, I3(*axes), I3(*grid), I3(*_three(origin, int)), F3(*_three(theta, float)),
+                              F3(*_three(pos_scale, float)), pairing, norm, eps, dtype, pos_per_batch, out_tokens,
+                              L3(ld, ld, ld), L3(batch, batch, batch), ld, batch)
+
+
+def _rope_rows(name, t, p, i):
+    """Checks the strides of one [B, N, H, d] or [N, H, d] tensor of rows and puts them into p."""
+    if t.stride(-1) != 1 or (p.H > 1 and t.stride(-2) != p.d):
+        raise ValueError(f"{name}: the heads of a token have to be dense")
+    p.ld[i] = t.stride(-3) if p.N > 1 else p.H * p.d
+    p.batch[i] = t.stride(0) if t.dim() == 4 and p.B > 1 else p.N * p.H * p.d
+
+
+def _rope_call(rows, wq, wk, axes, grid, positions, origin, theta, pos_scale, pairing, norm, eps, shape, dev, dtype,
+               out_tokens):
+    import torch
+    codes = {torch.bfloat16: SVGEAR_BF16, torch.float32: SVGEAR_F32}
+    if dtype not in codes:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if len(shape) not in (3, 4):
+        raise ValueError(f"rows [B, N, H, d] or [N, H, d] expected, got shape {tuple(shape)}")
+    B, (N, H, d) = (shape[0] if len(shape) == 4 else 1), shape[-3:]
+    p = rope_params(B, N, H, d, axes, grid if grid is not None else (0, 0, 0), origin, theta, pos_scale, pairing, norm,
+                    eps, codes[dtype], int(positions is not None and positions.dim() == 3), out_tokens)
+    for i, (name, t) in enumerate(rows):
+        if t is not None:
+            _want(name, t, dtype, shape, dev, contiguous=False)
+            _rope_rows(name, t, p, i)
+    cols = d if norm == SVGEAR_QKNORM_HEAD else H * d
+    _want("wq", wq, torch.float32, (cols,), dev)
+    _want("wk", wk, torch.float32, (cols,), dev)
+    _want("positions", positions, torch.int32, (B, N, 3) if p.pos_per_batch else (N, 3), dev)
+    return p
+
+
+def qkv_rope(q, k, v, *, axes, grid=None, positions=None, wq=None, wk=None, origin=0, theta=10000.0, pos_scale=1.0,
+             pairing: int = SVGEAR_PAIR_ADJACENT, norm: int = SVGEAR_QKNORM_NONE, eps: float = 1e-6, out=None,
+             out_at: int = 0, stream=None):
+    """Q, K, V [B*H, N, d] for the attention from projection rows [B, N, H, d] or [N, H, d] (views of a fused
+    projection may be passed), through svgear_qkv_rope: RMS norm of q and k, rotary positions on three axes,
+    head-major order.  Each of q, k, v may be None.  With out=(Q, K, V), tensors [B*H, M, d], the tokens go to
+    rows [out_at, out_at + N) and the others stay (a joint sequence, part by part).  Returns (Q, K, V)."""
+    import torch
+    given = [t for t in (q, k, v) if t is not None]
+    if not given:
+        raise ValueError("one of q, k, v expected")
+    x = given[0]
+    if not x.is_cuda:
+        raise ValueError("device tensor expected")
+    dev = x.device
+    M = x.shape[-3] if out is None else next(t.shape[1] for t in out if t is not None)
+    p = _rope_call((("q", q), ("k", k), ("v", v)), wq, wk, axes, grid, positions, origin, theta, pos_scale, pairing,
+                   norm, eps, x.shape, dev, x.dtype, M)
+    shape = (p.B * p.H, M, p.d)
+    with _On(dev, stream):
+        if out is None:
+            out = tuple(None if t is None else torch.empty(shape, dtype=x.dtype, device=dev) for t in (q, k, v))
+        if not 0 <= out_at <= M - p.N:
+            raise ValueError(f"out_at {out_at}: {p.N} tokens do not fit into {M} rows there")
+        for name, t in zip(("Q", "K", "V"), out):
+            _want(name, t, x.dtype, shape, dev)
+        dst = [None if t is None else t[:, out_at:] for t in out]
+        svgear_qkv_rope(q, k, v, wq, wk, positions, p, *dst)
+    return tuple(out)
+
+
+def qkv_rope_backward(dQ, dK, dV, q=None, k=None, *, axes, grid=None, positions=None, wq=None, wk=None, origin=0,
+                      theta=10000.0, pos_scale=1.0, pairing: int = SVGEAR_PAIR_ADJACENT,
+                      norm: int = SVGEAR_QKNORM_NONE, eps: float = 1e-6, H: Optional[int] = None, stream=None):
+    """Gradients of qkv_rope for the gradients of Q, K, V ([B*H, N, d], each may be None), through
+    svgear_qkv_rope_backward.  q and k are the forward's inputs; without them (no norm) H gives the heads.
+    dq, dk and dv are views [B, N, H, d] of one fused buffer [B, N, 3, H, d] ([N, H, d] when q or k has no
+    batch).  Returns a dict with dq, dk, dv, dwq, dwk; None for what was not given."""
+    import torch
+    given = [t for t in (dQ, dK, dV) if t is not None]
+    if not given:
+        raise ValueError("one of dQ, dK, dV expected")
+    g = given[0]
+    if not g.is_cuda or g.dim() != 3:
+        raise ValueError("gradients [B*H, N, d] on a device expected")
+    ref = q if q is not None else k
+    if ref is not None:
+        shape = tuple(ref.shape)
+    else:
+        if not H or g.shape[0] % H:
+            raise ValueError("H: the number of heads expected where q and k are not given")
+        shape = (g.shape[0] // H, g.shape[1], H, g.shape[2])
+    if norm != SVGEAR_QKNORM_NONE and ((dQ is not None and q is None) or (dK is not None and k is None)):
+        raise ValueError("q and k expected with a norm")
+    p = _rope_call((("q", q), ("k", k), ("v", None)), wq, wk, axes, grid, positions, origin, theta, pos_scale, pairing,
+                   norm, eps, shape, g.device, g.dtype, 0)
+    for name, t in (("dQ", dQ), ("dK", dK), ("dV", dV)):
+        _want(name, t, g.dtype, (p.B * p.H, p.N, p.d), g.device)
+    have = [i for i, t in enumerate((dQ, dK, dV)) if t is not None]
+    with _On(g.device, stream):
+        fused = torch.empty((p.B, p.N, len(have), p.H, p.d), dtype=g.dtype, device=g.device)
+        p.grad_ld, p.grad_batch = fused.stride(1), fused.stride(0)
+        rows = [None, None, None]
+        for at, i in enumerate(have):
+            rows[i] = fused[:, :, at] if len(shape) == 4 else fused[0, :, at]
+        like = lambda w, t: torch.empty_like(w) if w is not None and t is not None else None  # noqa: E731
+        dwq, dwk = like(wq, dQ), like(wk, dK)
+        ws = workspace(svgear_qkv_rope_backward_workspace_size(p), g.device) if dwq is not None or dwk is not None else None
+        svgear_qkv_rope_backward(dQ, dK, dV, q, k, wq, wk, positions, p, *rows, dwq, dwk, ws,
+                                 ws.numel() if ws is not None else 0)
+    return {"dq": rows[0], "dk": rows[1], "dv": rows[2], "dwq": dwq, "dwk": dwk}

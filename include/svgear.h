@@ -331,6 +331,132 @@ SVGEAR_API int svgear_forward(const void* Q, const void* K, const void* V, const
                    const float* init_q, const float* init_k, void* O, void* ws,
                    size_t ws_bytes, void* stream, svgear_stats* stats);
 
+/* ===========================================================================
+ * Around the attention: the rest of a video-DiT attention block, from the
+ * residual stream to Q, K, V and from O back to the residual stream
+ *   svgear_block_norm   -> projection -> svgear_qkv_rope -> svgear_forward
+ *   -> projection -> svgear_block_norm (with the block's output)
+ * with svgear_mx_* as the projections in 4 bits.  No counterpart in the
+ * paper.  The conventions above hold, with these differences: row lengths
+ * are as stated per call, and in-place use is as stated per call; any other
+ * overlap of an output with an input is not allowed.
+ * ======================================================================== */
+
+/* ---------------------------------------------------------------------------
+ * Gated residual with the norms before and after a block.  Per row n of group
+ * g (P, Q = norm of a row over its D columns, without weights):
+ *   m = P(y) post_weight          P = p->post
+ *   r = res_scale x + gate[g] m   (r = x when y is NULL)
+ *   h = (Q(r) weight + bias)(1 + scale[g]) + shift[g]    Q = p->pre
+ * Statistics are float32 over the whole row (mean first, then the squared
+ * deviations); h is formed from r before r is rounded to its type.
+ *   x, r  [N,D] in res_dtype; y, h [N,D] in dtype.  (res_dtype, dtype) is
+ *         (bf16, bf16), (f32, f32) or (f32, bf16).
+ *   gate, scale, shift [G,D], weight, bias, post_weight [D] float32; NULL
+ *         stands for 1, 0, 0, 1, 0, 1.
+ *   offsets [G+1] int32: group g is the rows [offsets[g], offsets[g+1]),
+ *         ascending from 0, empty groups allowed; rows from offsets[G] on are
+ *         left as they were.  NULL: G groups of N/G rows (N a multiple of G).
+ *         Values outside [0, N] are clamped.
+ *   y NULL: gate and post_weight NULL, post NONE, res_scale 1, r NULL.
+ *   h NULL: only r is formed.
+ * r may be x, and h may be y (or x when y is NULL) where the types agree.
+ * D a multiple of 8, at most 8192 (else SVGEAR_ERR_UNSUPPORTED); eps > 0.
+ * ------------------------------------------------------------------------- */
+typedef enum { SVGEAR_NORM_NONE = 0, SVGEAR_NORM_RMS = 1, SVGEAR_NORM_LAYER = 2 } svgear_norm;
+
+typedef struct {
+  int N, D, G;     /* rows, columns, groups of rows */
+  int pre, post;   /* svgear_norm of r (before the next block) and of y (after this one) */
+  float eps;       /* added to the mean square under the root */
+  float res_scale; /* factor of x in r */
+  int dtype;       /* svgear_dtype of y, h, dy, dh */
+  int res_dtype;   /* svgear_dtype of x, r, dx, dr */
+} svgear_norm_params;
+
+SVGEAR_API int svgear_block_norm(const void* x, const void* y, const float* gate, const float* scale,
+                      const float* shift, const float* weight, const float* bias,
+                      const float* post_weight, const int32_t* offsets,
+                      const svgear_norm_params* p, void* r, void* h, void* stream);
+
+/* Gradients of svgear_block_norm from dr [N,D] (res_dtype) and dh [N,D]
+ * (dtype), the gradients of r and h; one of the two may be NULL (zero).  The
+ * forward's inputs are given again; nothing else is kept from the forward.
+ *   dx [N,D] res_dtype, dy [N,D] dtype (NULL exactly when y is NULL),
+ *   dgate, dscale, dshift [G,D], dweight, dbias, dpost_weight [D] float32,
+ *   each NULL when not wanted (dgate and dpost_weight need y).
+ * Rows from offsets[G] on are neither read into a sum nor written.  The sums
+ * over rows are added in a fixed order (same bits on every call).
+ * dx may be x or dr, dy may be y or dh.
+ *   ws: svgear_block_norm_backward_workspace_size(p) bytes. */
+SVGEAR_API size_t svgear_block_norm_backward_workspace_size(const svgear_norm_params* p);
+SVGEAR_API int svgear_block_norm_backward(const void* x, const void* y, const void* dr, const void* dh,
+                      const float* gate, const float* scale, const float* weight,
+                      const float* bias, const float* post_weight, const int32_t* offsets,
+                      const svgear_norm_params* p, void* dx, void* dy, float* dgate,
+                      float* dscale, float* dshift, float* dweight, float* dbias,
+                      float* dpost_weight, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rows of a Q/K/V projection to the attention's operands: RMS norm of Q and K,
+ * rotary positions on three axes (time, height, width), and token-major to
+ * head-major order.
+ *   z = x | x / rms_head(x) w[d] | x / rms_token(x) w[H*d]   (p->norm)
+ *   pair (a, b) of z -> (a cos - b sin, a sin + b cos)
+ *   angle of pair i of axis A: pos_scale[A] (pos_A + origin[A]) theta[A]^(-2i/axes[A])
+ * axes[A] columns of every head turn with axis A, the axes one after another;
+ * columns behind them pass through.  Pair i of a head is the columns
+ * (2i, 2i+1) for SVGEAR_PAIR_ADJACENT, (i, i + d/2) for SVGEAR_PAIR_HALF.
+ * V is moved only.  Angles are reduced in float64.
+ *   q, k, v: element [b][n][h][t] at b*batch[i] + n*ld[i] + h*d + t (i = 0, 1,
+ *     2; strides in elements, rows 16-byte aligned); each may be NULL with
+ *     its output.
+ *   wq, wk: float32 [d] (HEAD) or [H*d] (TOKEN); NULL: 1.
+ *   positions: int32 [N][3], or [B][N][3] with pos_per_batch; NULL: token n <
+ *     grid[0]*grid[1]*grid[2] sits at its raster place in the grid (width
+ *     fastest), later tokens (text) do not turn.
+ *   Q, K, V out: [B*H][out_tokens][d], token n at row n of each head;
+ *     out_tokens 0 means N.  With out_tokens > N the rows behind are left as
+ *     they were, and a pointer moved by t*d places the tokens at row t: a
+ *     joint sequence is written by one call per part.
+ * d in {64, 128}, H*d <= 16384.
+ * ------------------------------------------------------------------------- */
+typedef enum { SVGEAR_PAIR_ADJACENT = 0, SVGEAR_PAIR_HALF = 1 } svgear_pairing;
+typedef enum { SVGEAR_QKNORM_NONE = 0, SVGEAR_QKNORM_HEAD = 1, SVGEAR_QKNORM_TOKEN = 2 } svgear_qknorm;
+
+typedef struct {
+  int B, N, H, d;      /* batch entries, tokens per entry, heads, head dimension */
+  int axes[3];         /* columns per head turned by each axis: even, sum <= d */
+  int grid[3];         /* frames, height, width (read when positions is NULL) */
+  int origin[3];       /* added to the positions */
+  float theta[3];      /* base of each axis, > 0 */
+  float pos_scale[3];  /* factor of each axis' positions */
+  int pairing, norm;   /* svgear_pairing, svgear_qknorm */
+  float eps;           /* of the norm, > 0 */
+  int dtype;           /* svgear_dtype of all rows */
+  int pos_per_batch;   /* positions are [B][N][3] */
+  int out_tokens;      /* tokens per head of Q, K, V (0: N) */
+  int64_t ld[3], batch[3];      /* strides of q, k, v, in elements */
+  int64_t grad_ld, grad_batch;  /* backward: strides of dq, dk and dv */
+} svgear_rope_params;
+
+SVGEAR_API int svgear_qkv_rope(const void* q, const void* k, const void* v, const float* wq,
+                      const float* wk, const int32_t* positions, const svgear_rope_params* p,
+                      void* Q, void* K, void* V, void* stream);
+
+/* Gradients of svgear_qkv_rope: dQ, dK, dV [B*H][out_tokens][d] give dq, dk,
+ * dv (element [b][n][h][t] at b*grad_batch + n*grad_ld + h*d + t; each NULL
+ * with its gradient) and dwq, dwk (NULL when not wanted).  q and k, the
+ * forward's inputs, are read only with a norm.
+ *   ws: svgear_qkv_rope_backward_workspace_size(p) bytes (0 without a norm;
+ *   not needed when dwq and dwk are NULL). */
+SVGEAR_API size_t svgear_qkv_rope_backward_workspace_size(const svgear_rope_params* p);
+SVGEAR_API int svgear_qkv_rope_backward(const void* dQ, const void* dK, const void* dV, const void* q,
+                      const void* k, const float* wq, const float* wk,
+                      const int32_t* positions, const svgear_rope_params* p, void* dq,
+                      void* dk, void* dv, float* dwq, float* dwk, void* ws,
+                      size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

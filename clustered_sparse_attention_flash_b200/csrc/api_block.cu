@@ -84,6 +84,22 @@ int check_rope_inputs(const void* const in[3], const float* wq, const float* wk,
   return SVGEAR_OK;
 }
 
+int check_mx(int M, int K) {
+  if (M < 1 || K < 1) return SVGEAR_ERR_INVALID;
+  if (K % 32 || K > (1 << 20)) return SVGEAR_ERR_UNSUPPORTED;
+  if ((long long)M * K >= (1LL << 39)) return SVGEAR_ERR_UNSUPPORTED;  // one block of 2,048 elements per grid index
+  return SVGEAR_OK;
+}
+
+int check_product(int M, int N, int K) {
+  int rc = check_mx(M, K);
+  if (!rc) rc = check_mx(N, K);
+  if (rc) return rc;
+  if (N % 8) return SVGEAR_ERR_UNSUPPORTED;
+  // tile indices are int
+  return ((long long)M / 16 + 1) * ((long long)N / 128 + 1) < (1LL << 31) ? SVGEAR_OK : SVGEAR_ERR_UNSUPPORTED;
+}
+
 }  // namespace
 }  // namespace svg
 
@@ -176,6 +192,38 @@ int svgear_qkv_rope_backward(const void* dQ, const void* dK, const void* dV, con
   if (!aligned16(dQ, dK, dV, dq, dk, dv, dwq, dwk)) return SVGEAR_ERR_INVALID;
   if ((dwq || dwk) && (!ws || !aligned16(ws) || ws_bytes < qkv_rope_back_ws_bytes(p))) return SVGEAR_ERR_WORKSPACE;
   return cuda_status(qkv_rope_back_run(grad, in, wq, wk, positions, p, out, dwq, dwk, ws, S(stream)));
+}
+
+int svgear_mx_quantize(const void* X, int dtype, int M, int K, int head_d, uint8_t* codes, uint8_t* scales, void* stream) {
+  const int rc = check_mx(M, K);
+  if (rc) return rc;
+  if (!known_dtype(dtype)) return SVGEAR_ERR_UNSUPPORTED;
+  if (head_d < 0 || (head_d && (head_d % 8 || K % head_d))) return SVGEAR_ERR_INVALID;
+  if (!X || !codes || !scales || !aligned16(X, codes, scales)) return SVGEAR_ERR_INVALID;
+  return cuda_status(mx_quantize_run(X, dtype, M, K, head_d, codes, scales, S(stream)));
+}
+
+int svgear_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int M, int K, void* Y, int dtype, void* stream) {
+  const int rc = check_mx(M, K);
+  if (rc) return rc;
+  if (!known_dtype(dtype)) return SVGEAR_ERR_UNSUPPORTED;
+  if (!Y || !codes || !scales || !aligned16(Y, codes, scales)) return SVGEAR_ERR_INVALID;
+  return cuda_status(mx_dequantize_run(codes, scales, M, K, Y, dtype, S(stream)));
+}
+
+size_t svgear_mx_product_workspace_size(int M, int N, int K) {
+  return check_product(M, N, K) ? 0 : mx_product_ws_bytes(M, N, K);
+}
+
+int svgear_mx_product(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes, const uint8_t* w_scales,
+                      const float* bias, int M, int N, int K, void* Y, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_product(M, N, K);
+  if (rc) return rc;
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !Y) return SVGEAR_ERR_INVALID;
+  if (!aligned16(a_codes, a_scales, w_codes, w_scales, bias, Y)) return SVGEAR_ERR_INVALID;
+  const size_t need = mx_product_ws_bytes(M, N, K);
+  if (need && (!ws || !aligned16(ws) || ws_bytes < need)) return SVGEAR_ERR_WORKSPACE;
+  return cuda_status(mx_product_run(a_codes, a_scales, w_codes, w_scales, bias, M, N, K, Y, ws, S(stream)));
 }
 
 }  // extern "C"

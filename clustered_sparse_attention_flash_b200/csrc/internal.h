@@ -96,6 +96,15 @@ cudaError_t qkv_rope_back_run(const void* const grad[3], const void* const in[2]
                               const int32_t* pos, const svgear_rope_params* p, void* const out[3], float* dwq, float* dwk,
                               void* ws, cudaStream_t st);
 
+// ---- microscaled 4-bit floats (mx_quant.cu, mx_product.cu)
+cudaError_t mx_quantize_run(const void* X, int dtype, int M, int K, int head_d, uint8_t* codes, uint8_t* scales,
+                            cudaStream_t st);
+cudaError_t mx_dequantize_run(const uint8_t* codes, const uint8_t* scales, int M, int K, void* Y, int dtype,
+                              cudaStream_t st);
+size_t mx_product_ws_bytes(int M, int N, int K);
+cudaError_t mx_product_run(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes, const uint8_t* w_scales,
+                           const float* bias, int M, int N, int K, void* Y, void* ws, cudaStream_t st);
+
 // ---- TMA tensor maps (tma_host.cu)
 constexpr int kTmaMapBytes = 128;
 bool tma_available();
@@ -104,6 +113,10 @@ bool tma_available();
 // 64-byte aligned).  Out-of-range rows read as zeros.  False when the driver
 // entry point is missing or the arguments are not encodable.
 bool tma_map_bf16_3d(void* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box1);
+
+// Tiled map of dense byte rows [rows][row_bytes] with box {128 bytes, box_rows}
+// and 128-byte swizzle; what lies outside reads as zeros.
+bool tma_map_u8_rows(void* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

@@ -49,4 +49,18 @@ bool tma_map_bf16_3d(void* map, const void* base, uint64_t d0, uint64_t d1, uint
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tma_map_u8_rows(void* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows) {
+  EncodeTiled fn = encode_fn();
+  if (!fn || (reinterpret_cast<uintptr_t>(base) & 15u) || row_bytes % 16 || row_bytes == 0 || rows == 0 || box_rows == 0 ||
+      box_rows > 256)
+    return false;
+  const cuuint64_t dims[3] = {row_bytes, rows, 1};
+  const cuuint64_t strides[2] = {row_bytes, row_bytes * rows};
+  const cuuint32_t box[3] = {128, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace svg

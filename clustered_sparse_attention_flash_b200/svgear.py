@@ -121,6 +121,10 @@ _SIGS = {
     "svgear_qkv_rope": (_I, [_P] * 6 + [_RP] + [_P] * 4),
     "svgear_qkv_rope_backward_workspace_size": (_SZ, [_RP]),
     "svgear_qkv_rope_backward": (_I, [_P] * 8 + [_RP] + [_P] * 6 + [_SZ, _P]),
+    "svgear_mx_quantize": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
+    "svgear_mx_dequantize": (_I, [_P, _P, _I, _I, _P, _I, _P]),
+    "svgear_mx_product_workspace_size": (_SZ, [_I, _I, _I]),
+    "svgear_mx_product": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _SZ, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -329,6 +333,26 @@ def svgear_qkv_rope_backward(dQ, dK, dV, q, k, wq, wk, positions, p, dq, dk, dv,
         _rows_ptr(dQ), _rows_ptr(dK), _rows_ptr(dV), _rows_ptr(q), _rows_ptr(k), _ptr(wq), _ptr(wk),
         _ptr(positions), ctypes.byref(p), _rows_ptr(dq), _rows_ptr(dk), _rows_ptr(dv), _ptr(dwq), _ptr(dwk),
         _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def svgear_mx_quantize(X, dtype, M, K, head_d, codes, scales, stream=None):
+    _check("svgear_mx_quantize", lib().svgear_mx_quantize(
+        _ptr(X), dtype, M, K, head_d, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def svgear_mx_dequantize(codes, scales, M, K, Y, dtype, stream=None):
+    _check("svgear_mx_dequantize", lib().svgear_mx_dequantize(
+        _ptr(codes), _ptr(scales), M, K, _ptr(Y), dtype, _stream(stream)))
+
+
+def svgear_mx_product_workspace_size(M, N, K) -> int:
+    return lib().svgear_mx_product_workspace_size(M, N, K)
+
+
+def svgear_mx_product(a_codes, a_scales, w_codes, w_scales, bias, M, N, K, Y, ws, ws_bytes, stream=None):
+    _check("svgear_mx_product", lib().svgear_mx_product(
+        _ptr(a_codes), _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), _ptr(bias), M, N, K, _ptr(Y), _ptr(ws),
+        ws_bytes, _stream(stream)))
 
 
 # ------------------------------------------------------- torch conveniences
@@ -638,3 +662,57 @@ def qkv_rope_backward(dQ, dK, dV, q=None, k=None, *, axes, grid=None, positions=
         svgear_qkv_rope_backward(dQ, dK, dV, q, k, wq, wk, positions, p, *rows, dwq, dwk, ws,
                                  ws.numel() if ws is not None else 0)
     return {"dq": rows[0], "dk": rows[1], "dv": rows[2], "dwq": dwq, "dwk": dwk}
+
+
+def mx_quantize(x, stream=None):
+    """(codes [M, K/2], scales [M, K/32]), uint8, of x [M, K] or of the attention's head-major output
+    [H, M, d] (K = H d), through svgear_mx_quantize."""
+    import torch
+    if not x.is_cuda:
+        raise ValueError("x: device tensor expected")
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x: [M, K] or [H, M, d] expected, got shape {tuple(x.shape)}")
+    M, K, head_d = (x.shape[0], x.shape[1], 0) if x.dim() == 2 else (x.shape[1], x.shape[0] * x.shape[2], x.shape[2])
+    with _On(x.device, stream):
+        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
+        svgear_mx_quantize(x, dtype_code(x), M, K, head_d, codes, scales)
+    return codes, scales
+
+
+def mx_dequantize(codes, scales, dtype=None, stream=None):
+    """The values [M, K] of codes and scales in `dtype` (default torch.bfloat16), through svgear_mx_dequantize."""
+    import torch
+    M, K = codes.shape[0], codes.shape[1] * 2
+    _want("codes", codes, torch.uint8, (M, K // 2), codes.device)
+    _want("scales", scales, torch.uint8, (M, K // 32), codes.device)
+    with _On(codes.device, stream):
+        y = torch.empty((M, K), dtype=dtype or torch.bfloat16, device=codes.device)
+        svgear_mx_dequantize(codes, scales, M, K, y, dtype_code(y))
+    return y
+
+
+def mx_product(a_codes, a_scales, w_codes, w_scales, bias=None, stream=None):
+    """Y [M, N] bfloat16 = A W^T + bias for MXFP4 A [M, K] and W [N, K], through svgear_mx_product."""
+    import torch
+    M, N, K = a_codes.shape[0], w_codes.shape[0], w_codes.shape[1] * 2
+    dev = a_codes.device
+    _want("a_codes", a_codes, torch.uint8, (M, K // 2), dev)
+    _want("a_scales", a_scales, torch.uint8, (M, K // 32), dev)
+    _want("w_codes", w_codes, torch.uint8, (N, K // 2), dev)
+    _want("w_scales", w_scales, torch.uint8, (N, K // 32), dev)
+    _want("bias", bias, torch.float32, (N,), dev)
+    with _On(dev, stream):
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        need = svgear_mx_product_workspace_size(M, N, K)
+        ws = workspace(need, dev) if need else None
+        svgear_mx_product(a_codes, a_scales, w_codes, w_scales, bias, M, N, K, y, ws, need)
+    return y
+
+
+def mx_linear(x, w_codes, w_scales, bias=None, stream=None):
+    """Y [M, N] bfloat16 = quantised x times W^T + bias: mx_quantize, then mx_product."""
+    if x.dim() == 2 and x.shape[1] != 2 * w_codes.shape[1]:
+        raise ValueError(f"x: {2 * w_codes.shape[1]} columns expected, got shape {tuple(x.shape)}")
+    codes, scales = mx_quantize(x, stream)
+    return mx_product(codes, scales, w_codes, w_scales, bias, stream)

@@ -457,6 +457,39 @@ SVGEAR_API int svgear_qkv_rope_backward(const void* dQ, const void* dK, const vo
                       void* dk, void* dv, float* dwq, float* dwk, void* ws,
                       size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Microscaled 4-bit floats (OCP Microscaling Formats v1.0, MXFP4): blocks of 32
+ * consecutive elements of a row, E2M1 elements under one E8M0 scale
+ * 2^(byte-127).
+ *   codes [M][K/2]: two elements per byte, the even one in the low four bits;
+ *   scales [M][K/32] bytes.  K a multiple of 32.
+ * Quantisation (section 6.3 of the specification): scale exponent
+ * floor(log2 amax) - 2 clamped to the format's range, elements rounded to
+ * nearest even, magnitudes above 6 scales saturate.  A block that holds a NaN
+ * or an infinity gets scale byte 255 (NaN) and zero codes.
+ *   X [M][K], or head-major [K/head_d][M][head_d] when head_d > 0 (the
+ *   attention's output, joined to rows on the way): head_d a multiple of 8
+ *   that divides K.
+ * ------------------------------------------------------------------------- */
+SVGEAR_API int svgear_mx_quantize(const void* X, int dtype, int M, int K, int head_d, uint8_t* codes,
+                      uint8_t* scales, void* stream);
+
+/* Y [M][K] (dtype): the values that codes and scales stand for (exact in
+ * float32 and, for scale bytes above 1, in bfloat16). */
+SVGEAR_API int svgear_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int M, int K, void* Y,
+                      int dtype, void* stream);
+
+/* Y[m][n] = sum_k A[m][k] W[n][k] + bias[n], Y [M][N] bfloat16: tokens A [M][K]
+ * times weights W [N][K], both MXFP4 as above.  Products are exact, sums are
+ * float32, rounded once; a NaN scale makes its row (column) of Y NaN.
+ *   bias [N] float32 or NULL.  N a multiple of 8, K a multiple of 32.
+ *   ws: svgear_mx_product_workspace_size(M, N, K) bytes (may be 0, then NULL
+ *   will do). */
+SVGEAR_API size_t svgear_mx_product_workspace_size(int M, int N, int K);
+SVGEAR_API int svgear_mx_product(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
+                      const uint8_t* w_scales, const float* bias, int M, int N, int K, void* Y,
+                      void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

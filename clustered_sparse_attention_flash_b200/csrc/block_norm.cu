@@ -5,23 +5,23 @@
 //   n = Q(r),  h = (n w + b)(1 + s) + t
 //
 // One pass: a row is loaded once into registers, its statistics are taken
-// there (mean first, then the squared deviations, so nothing cancels), and r
-// and h leave from the same registers.  h is formed from the unrounded r.
+// there, and r and h leave from the same registers.  h is formed from the unrounded r.
 // The per-column coefficients (1+s) w, b (1+s) + t and g w2 stay in registers
 // while consecutive rows belong to one group.
 //
 // A row is owned by a worker: 8, 16 or 32 lanes of a warp for D <= 256,
-// otherwise a whole block (one 8-element vector per thread, two above 5,120
-// columns).  A worker walks a contiguous run of rows, so column sums of the
+// otherwise a whole block (two 8-element vectors per thread).  A worker walks a contiguous run of rows, so column sums of the
 // backward pass stay in registers until the group or the run ends; partial
 // sums then go to slot (worker + group), which no other pair maps to because
 // both only grow along the rows, and are added in slot order: no atomics, the
 // same bits every time.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
 #include "rowvec.cuh"
+#include "tc_common.cuh"
 
 namespace svg {
 
@@ -31,10 +31,11 @@ struct NormArgs {
   const void *x, *y, *dr, *dh;
   const float *gate, *scale, *shift, *weight, *bias, *post_weight;
   const int32_t* offsets;
-  int N, D, G, pre, post, tpr, chunk;
+  int N, D, G, pre, post, tpr, chunk, stages, ring_bytes;
   float eps, a;
   void *r, *h, *dx, *dy;
   float* part;  // backward: [slots][3][D] partial column sums
+  int* status;
 };
 
 // First row behind group g (offsets are clamped, so bad ones stay in range).
@@ -53,324 +54,526 @@ __device__ __forceinline__ int group_of(const NormArgs& p, int row) {
   return lo;
 }
 
-// Row statistics of f (inactive vectors hold zeros): f becomes the normalised
-// row, the return value is 1 / deviation.  The deviations from the rounded
-// mean sum to D times what the mean is off, which the second sum carries along
-// with the squares: mean and variance are both corrected by it.  A constant
-// row of a large value would otherwise show its mean's last bit, magnified by
-// 1/sqrt(eps).
+// What a thread knows of its row: which of its V vectors exist, and the number
+// of columns of its warp and of the warp whose totals RowSum::trade hands it.
 template <int V>
-__device__ __forceinline__ float normalise(float (&f)[V][kVec], const bool (&on)[V], int kind, float d, float eps,
-                                           RowSum& sum) {
-  if (kind == SVGEAR_NORM_NONE) return 1.f;
-  float2 q = make_float2(0.f, 0.f);
-  if (kind == SVGEAR_NORM_LAYER) {
-    float s = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) s += f[v][i];
-    const float mean = sum(s) / d;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        f[v][i] = on[v] ? f[v][i] - mean : 0.f;
-        q.y += f[v][i];
-      }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) q.x = fmaf(f[v][i], f[v][i], q.x);
-  q = sum(q);
-  const float off = q.y / d;  // 0 for an RMS norm
-  const float inv = rsqrtf(fmaxf(fmaf(-off, off, q.x / d), 0.f) + eps);
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) f[v][i] = on[v] ? (f[v][i] - off) * inv : 0.f;
-  return inv;
-}
-
-template <typename TX, typename TY, int V>
-__global__ void __launch_bounds__(V == 1 ? 640 : 512) k_block_norm(const NormArgs p) {
-  __shared__ float2 scratch[64];
-  RowSum sum{scratch, p.tpr, 0};
-  const int slot = threadIdx.x / p.tpr, lane = threadIdx.x - slot * p.tpr;
-  const long long worker = (long long)blockIdx.x * (blockDim.x / p.tpr) + slot;
-  const float d = (float)p.D;
-  long long row = worker * p.chunk;
-  const long long end = row + p.chunk < p.N ? row + p.chunk : p.N;
-  const TX* x = static_cast<const TX*>(p.x);
-  const TY* y = static_cast<const TY*>(p.y);
+struct Columns {
   int col[V];
   bool on[V];
+  float inv_d, d, inv_own, n, inv_n;
+  __device__ __forceinline__ void init(int D, int tpr, int lane, const RowSum& sum) {
+    d = (float)D;
+    inv_d = 1.f / d;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      col[v] = (v * tpr + lane) * kVec;
+      on[v] = col[v] < D;
+    }
+    auto columns_of = [&](int w) {
+      int c = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) c += max(0, min(D - (v * tpr + 32 * w) * kVec, 32 * kVec));
+      return (float)c;
+    };
+    const float own = tpr > 32 ? columns_of(lane >> 5) : d;
+    inv_own = own > 0.f ? 1.f / own : 0.f;
+    const int other = threadIdx.x & sum.mask;
+    n = tpr > 32 && other < tpr >> 5 ? columns_of(other) : 0.f;
+    inv_n = n > 0.f ? 1.f / n : 0.f;
+  }
+};
+
+template <int V>
+__device__ __forceinline__ float total(const Vec (&f)[V], const Columns<V>& c) {
+  float s = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    col[v] = (v * p.tpr + lane) * kVec;
-    on[v] = col[v] < p.D;
+    const float2 h = halves(add2(add2(f[v].v[0], f[v].v[1]), add2(f[v].v[2], f[v].v[3])));
+    s += c.on[v] ? h.x + h.y : 0.f;
   }
-  int g = row < end ? group_of(p, (int)row) : p.G;
-  long long gend = row;  // forces the first coefficient load
-  bool first = true;
-  float ca[V][kVec], cb[V][kVec], cg[V][kVec];
-  Raw<TX> xr[V];
-  Raw<TY> yr[V];
-  auto fetch = [&](long long rw) {
+  return s;
+}
+
+// Sum of (f - mean)^2 over this thread's columns.
+template <int V>
+__device__ __forceinline__ float squares(const Vec (&f)[V], const Columns<V>& c, float mean) {
+  float s = 0.f;
+  const f2 m = pair(-mean);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    f2 q = pair(0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f2 e = add2(f[v].v[i], m);
+      q = fma2(e, e, q);
+    }
+    const float2 h = halves(q);
+    s += c.on[v] ? h.x + h.y : 0.f;
+  }
+  return s;
+}
+
+// s / d rounded like a division, so that a constant row's mean is its value.
+__device__ __forceinline__ float over(float s, float d, float inv_d) {
+  const float q = s * inv_d;
+  return fmaf(fmaf(-q, d, s), inv_d, q);
+}
+
+// Mean and 1/deviation of a row with one barrier: a warp takes the mean and the
+// squared deviations of its own columns, and the warps' pairs (sum, squares)
+// are joined by
+//   squares = sum_w squares_w + n_w (mean_w - mean)^2,
+// every term of which is a square: nothing cancels, whatever the mean.
+template <int V>
+__device__ __forceinline__ float2 statistics(const Vec (&f)[V], const Columns<V>& c, int kind, float eps, RowSum& sum) {
+  if (kind == SVGEAR_NORM_RMS) return make_float2(0.f, rsqrtf(fmaf(sum(squares(f, c, 0.f)), c.inv_d, eps)));
+  const float s = sum.lanes(total(f, c));
+  if (sum.width <= 32) {
+    const float mean = over(s, c.d, c.inv_d);
+    return make_float2(mean, rsqrtf(fmaf(sum.lanes(squares(f, c, mean)), c.inv_d, eps)));
+  }
+  const float q = sum.lanes(squares(f, c, s * c.inv_own));
+  const float2 v = sum.trade(make_float2(s, q));
+  const float mean = over(sum.warps(v.x), c.d, c.inv_d), e = v.x * c.inv_n - mean;
+  return make_float2(mean, rsqrtf(fmaf(sum.warps(fmaf(c.n * e, e, v.y)), c.inv_d, eps)));
+}
+
+// f becomes the normalised row; returns 1 / deviation.
+template <int V>
+__device__ __forceinline__ float normalise(Vec (&f)[V], const Columns<V>& c, int kind, float eps, RowSum& sum) {
+  if (kind == SVGEAR_NORM_NONE) return 1.f;
+  const float2 st = statistics(f, c, kind, eps, sum);
+  const f2 m = pair(-st.x), inv = pair(st.y);
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[v].v[i] = mul2(add2(f[v].v[i], m), inv);
+  return st.y;
+}
+
+// Rows of a worker, one at a time, behind one interface: narrow rows straight
+// from global memory (the next row is loaded while this one is computed), wide
+// rows through a ring of bulk copies in shared memory, so that the bytes in
+// flight do not depend on how many threads are resident.  `take` fills the
+// vectors of this thread with its columns of `row`; rows come in order.  An
+// operand that is not given, or a column that does not exist, reads as zeros.
+template <typename TX, typename TY, int V>
+struct Row {
+  Raw<TX> x[V], dr[V];
+  Raw<TY> y[V], dh[V];
+};
+
+template <typename TX, typename TY, int OPS, int V>
+struct Direct {
+  const NormArgs& p;
+  const Columns<V>& c;
+  long long end;
+  Row<TX, TY, V> next;
+  template <typename T>
+  __device__ __forceinline__ void one(Raw<T>& r, const void* base, long long at, bool ok) {
+    zero_raw(r);
+    if (ok && base) load_raw(r, static_cast<const T*>(base) + at);
+  }
+  __device__ __forceinline__ void load(long long row) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const bool ok = on[v] && rw < end;
-      zero_raw(xr[v]);
-      if (ok) load_raw(xr[v], x + rw * p.D + col[v]);
-      if (y) {
-        zero_raw(yr[v]);
-        if (ok) load_raw(yr[v], y + rw * p.D + col[v]);
+      const long long at = row * p.D + c.col[v];
+      const bool ok = c.on[v] && row < end;
+      one(next.x[v], p.x, at, ok);
+      one(next.y[v], p.y, at, ok);
+      if (OPS == 4) {
+        one(next.dr[v], p.dr, at, ok);
+        one(next.dh[v], p.dh, at, ok);
       }
     }
-  };
-  fetch(row);
-  for (int it = 0; it < p.chunk; ++it, ++row) {
-    // rows of this worker are done, or lie behind the last group; whole blocks leave together
-    if (g < p.G && row < end && (first || row >= gend)) {
-      while (g < p.G && (gend = group_end(p, g)) <= row) ++g;
-      first = false;
-      if (g < p.G) {
+  }
+  __device__ __forceinline__ Direct(const NormArgs& args, const Columns<V>& cols, long long first, long long last)
+      : p(args), c(cols), end(last) {
+    load(first);
+  }
+  __device__ __forceinline__ void take(long long row, Row<TX, TY, V>& r) {
+    r = next;
+    load(row + 1);
+  }
+  __device__ __forceinline__ void release(long long) {}
+};
+
+constexpr int kMaxStages = 16;
+
+template <typename TX, typename TY, int OPS, int V>
+struct Ring {
+  const NormArgs& p;
+  const Columns<V>& c;
+  long long end;
+  uint32_t bx, by, stage;  // bytes of a row of either type, of a stage
+  uint8_t* buf;
+  uint64_t* full;
+  volatile int* abort_flag;
+  int slot;         // the stage of the row that is next taken,
+  uint32_t parity;  // and the parity of its phase
+  // One thread: the copies of `row` into stage s.
+  __device__ __forceinline__ void issue(long long row, int s) {
+    if (row >= end) return;
+    tc::mbar_arrive_expect_tx(full + s, bx + (p.y ? by : 0u) + (OPS == 4 ? (p.dr ? bx : 0u) + (p.dh ? by : 0u) : 0u));
+    const uint32_t dst = tc::smem_u32(buf) + s * stage;
+    tc::bulk_g2s(dst, static_cast<const char*>(p.x) + row * bx, bx, full + s);
+    if (p.y) tc::bulk_g2s(dst + bx, static_cast<const char*>(p.y) + row * by, by, full + s);
+    if (OPS == 4) {
+      if (p.dr) tc::bulk_g2s(dst + bx + by, static_cast<const char*>(p.dr) + row * bx, bx, full + s);
+      if (p.dh) tc::bulk_g2s(dst + 2 * bx + by, static_cast<const char*>(p.dh) + row * by, by, full + s);
+    }
+  }
+  __device__ __forceinline__ Ring(const NormArgs& args, const Columns<V>& cols, long long first, long long last)
+      : p(args), c(cols), end(last), slot(0), parity(0) {
+    extern __shared__ __align__(128) uint8_t dyn[];
+    __shared__ uint64_t bars[kMaxStages];
+    __shared__ int flag;
+    bx = p.D * sizeof(TX);
+    by = p.D * sizeof(TY);
+    stage = (OPS / 2) * (bx + by);
+    buf = dyn;
+    full = bars;
+    abort_flag = &flag;
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < p.stages; ++i) tc::mbar_init(full + i, 1);
+      flag = 0;
+      tc::mbar_fence_init();
+      for (int i = 0; i < p.stages; ++i) issue(first + i, i);
+    }
+    __syncthreads();
+  }
+  template <typename T>
+  __device__ __forceinline__ void one(Raw<T>& r, const void* base, const uint8_t* at, int v) {
+    zero_raw(r);
+    if (c.on[v] && base) r = *reinterpret_cast<const Raw<T>*>(at + c.col[v] * sizeof(T));
+  }
+  __device__ __forceinline__ void take(long long row, Row<TX, TY, V>& r) {
+    // A wait that gives up records it; the block goes on with what is there, so every thread still meets every barrier.
+    tc::mbar_wait(full + slot, parity, abort_flag, p.status);
+    const uint8_t* at = buf + slot * stage;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float w[kVec], t[kVec];
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) { ca[v][i] = 1.f; cb[v][i] = 0.f; cg[v][i] = 1.f; }
-          if (!on[v]) continue;
-          const size_t at = (size_t)g * p.D + col[v];
-          if (p.scale) {
-            load_f8(t, p.scale + at);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) ca[v][i] += t[i];
-          }
-          if (p.bias) {
-            load_f8(w, p.bias + col[v]);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) cb[v][i] = w[i] * ca[v][i];
-          }
-          if (p.shift) {
-            load_f8(t, p.shift + at);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) cb[v][i] += t[i];
-          }
-          if (p.weight) {
-            load_f8(w, p.weight + col[v]);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) ca[v][i] *= w[i];
-          }
-          if (p.gate) load_f8(cg[v], p.gate + at);
-          if (p.post_weight) {
-            load_f8(w, p.post_weight + col[v]);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) cg[v][i] *= w[i];
-          }
-        }
+    for (int v = 0; v < V; ++v) {
+      one(r.x[v], p.x, at, v);
+      one(r.y[v], p.y, at + bx, v);
+      if (OPS == 4) {
+        one(r.dr[v], p.dr, at + bx + by, v);
+        one(r.dh[v], p.dh, at + 2 * bx + by, v);
       }
     }
-    const bool live = g < p.G && row < end;
+  }
+  // Behind a barrier that follows take(row): the stage is free for a later row.
+  __device__ __forceinline__ void release(long long row) {
+    if (threadIdx.x == 0) issue(row + p.stages, slot);
+    if (++slot == p.stages) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+// The worker of a thread and its rows, up to the last group's end.
+struct Place {
+  long long worker, row, end;
+  int lane;
+};
+__device__ __forceinline__ Place place(const NormArgs& p) {
+  Place q;
+  const int slot = threadIdx.x / p.tpr;
+  q.worker = (long long)blockIdx.x * (blockDim.x / p.tpr) + slot;
+  q.lane = threadIdx.x - slot * p.tpr;
+  q.row = q.worker * p.chunk;
+  q.end = min(q.row + p.chunk, (long long)group_end(p, p.G - 1));
+  return q;
+}
+
+// The coefficients of this thread's columns in group g: (1 + scale) weight,
+// bias (1 + scale) + shift, gate post_weight.  Narrow rows keep them in
+// registers; wide rows keep all but the first in shared memory, each thread its
+// own columns: as registers they would cost the second block per SM (or spill
+// to local memory, which has no L1 left beside the ring: 879 us against 632 at
+// 75,600 x 5,120).
+template <int V, bool SHARED>
+struct Coefficients;
+template <int V>
+struct Coefficients<V, false> {
+  Vec a[V], b[V], g[V];
+  __device__ __forceinline__ Coefficients(const NormArgs&, const Columns<V>&, uint8_t*) {}
+  __device__ __forceinline__ void put(int which, int v, const Vec& t) { (which == 0 ? b : g)[v] = t; }
+  __device__ __forceinline__ Vec get_b(int v) const { return b[v]; }
+  __device__ __forceinline__ Vec get_g(int v) const { return g[v]; }
+};
+template <int V>
+struct Coefficients<V, true> {
+  Vec a[V];
+  float* at[V];
+  int D;
+  __device__ __forceinline__ Coefficients(const NormArgs& p, const Columns<V>& c, uint8_t* mem) : D(p.D) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) at[v] = reinterpret_cast<float*>(mem) + (c.on[v] ? c.col[v] : 0);
+  }
+  __device__ __forceinline__ void put(int which, int v, const Vec& t) { store_vec(at[v] + which * D, t); }
+  __device__ __forceinline__ Vec get_b(int v) const { Vec t; load_vec(t, at[v]); return t; }
+  __device__ __forceinline__ Vec get_g(int v) const { Vec t; load_vec(t, at[v] + D); return t; }
+};
+
+template <int V, bool SHARED>
+__device__ __forceinline__ void load_coefficients(const NormArgs& p, int g, const Columns<V>& c, Coefficients<V, SHARED>& k,
+                                                  bool want_b) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (!c.on[v]) continue;
+    const size_t at = (size_t)g * p.D + c.col[v];
+    Vec a, o, t;
+    fill(a, 1.f);
+    if (p.scale) {
+      load_vec(t, p.scale + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a.v[i] = add2(a.v[i], t.v[i]);
+    }
+    if (want_b) {
+      fill(o, 0.f);
+      if (p.bias) {
+        load_vec(t, p.bias + c.col[v]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o.v[i] = mul2(t.v[i], a.v[i]);
+      }
+      if (p.shift) {
+        load_vec(t, p.shift + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o.v[i] = add2(o.v[i], t.v[i]);
+      }
+      k.put(0, v, o);
+    }
+    if (p.weight) {
+      load_vec(t, p.weight + c.col[v]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a.v[i] = mul2(a.v[i], t.v[i]);
+    }
+    k.a[v] = a;
+    fill(o, 1.f);
+    if (p.gate) load_vec(o, p.gate + at);
+    if (p.post_weight) {
+      load_vec(t, p.post_weight + c.col[v]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o.v[i] = mul2(o.v[i], t.v[i]);
+    }
+    k.put(1, v, o);
+  }
+}
+
+// Block classes: vectors per thread, most threads of a block, and the threads
+// an SM is to hold (the launch bounds set the registers, the grid and the ring
+// count on them).  0: rows of up to 256 columns; 1, 2, 3: up to 2,048, 5,120
+// and 8,192 columns, two vectors per thread.
+template <int CLS, bool BACK>
+struct Class {
+  static constexpr int kV = CLS == 0 ? 1 : 2;
+  static constexpr int kMax = CLS == 0 ? 128 : CLS == 1 ? 128 : CLS == 2 ? 320 : 512;
+  static constexpr int kThreads = CLS == 0 ? (BACK ? 512 : 768) : CLS == 1 ? (BACK ? 384 : 640) : CLS == 2 ? (BACK ? 320 : 640) : 512;
+};
+
+// Shared memory of the wide rows: the ring's stages, then two coefficients per column.
+__device__ __forceinline__ uint8_t* coefficient_memory(const NormArgs& p) {
+  extern __shared__ __align__(128) uint8_t dyn[];
+  return dyn + p.ring_bytes;
+}
+
+template <typename TX, typename TY, int CLS>
+__global__ void __launch_bounds__(Class<CLS, false>::kMax, (Class<CLS, false>::kThreads / Class<CLS, false>::kMax))
+    k_block_norm(const __grid_constant__ NormArgs p) {
+  constexpr int V = Class<CLS, false>::kV;
+  __shared__ float2 scratch[64];
+  RowSum sum(scratch, p.tpr);
+  const Place pl = place(p);
+  Columns<V> c;
+  c.init(p.D, p.tpr, pl.lane, sum);
+  typename std::conditional<CLS == 0, Direct<TX, TY, 2, V>, Ring<TX, TY, 2, V>>::type rows(p, c, pl.row, pl.end);
+  int g = pl.row < pl.end ? group_of(p, (int)pl.row) : 0;
+  long long gend = pl.row;  // the first row loads the coefficients
+  // a sum over the block is the barrier behind which a stage is free
+  const bool barrier = (p.y && p.post != SVGEAR_NORM_NONE) || (p.h && p.pre != SVGEAR_NORM_NONE);
+  Coefficients<V, CLS != 0> k(p, c, coefficient_memory(p));
+  TX* r_out = static_cast<TX*>(p.r) + pl.row * p.D;
+  TY* h_out = static_cast<TY*>(p.h) + pl.row * p.D;
+  for (int it = 0; it < p.chunk; ++it, r_out += p.D, h_out += p.D) {
+    const long long row = pl.row + it;
+    const bool live = row < pl.end;
     if (p.tpr >= 32 && !live) break;  // uniform over the worker, which is whole warps
-    float f[V][kVec], m[V][kVec];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      unpack(xr[v], f[v]);
-      if (y) unpack(yr[v], m[v]);
+    if (live && row >= gend) {
+      while ((gend = group_end(p, g)) <= row && g + 1 < p.G) ++g;
+      load_coefficients(p, g, c, k, true);
     }
-    fetch(row + 1);
-    if (y) {
-      normalise<V>(m, on, p.post, d, p.eps, sum);
+    Row<TX, TY, V> in;
+    rows.take(row, in);
+    Vec f[V], m[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) unpack(in.x[v], f[v]);
+    if (p.y) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) unpack(in.y[v], m[v]);
+      normalise<V>(m, c, p.post, p.eps, sum);
+      const f2 a = pair(p.a);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
+        const Vec cg = k.get_g(v);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) f[v][i] = on[v] ? fmaf(p.a, f[v][i], cg[v][i] * m[v][i]) : 0.f;
-        if (live && on[v]) store_vec(static_cast<TX*>(p.r) + row * p.D + col[v], f[v]);
+        for (int i = 0; i < 4; ++i) f[v].v[i] = fma2(a, f[v].v[i], mul2(cg.v[i], m[v].v[i]));
+        if (live && c.on[v]) store_vec(r_out + c.col[v], f[v]);
       }
     }
     if (p.h) {
-      normalise<V>(f, on, p.pre, d, p.eps, sum);
+      const float2 st = p.pre == SVGEAR_NORM_NONE ? make_float2(0.f, 1.f) : statistics<V>(f, c, p.pre, p.eps, sum);
+      const f2 mean = pair(-st.x), inv = pair(st.y);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
+        const Vec cb = k.get_b(v);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) f[v][i] = fmaf(f[v][i], ca[v][i], cb[v][i]);
-        if (live && on[v]) store_vec(static_cast<TY*>(p.h) + row * p.D + col[v], f[v]);
+        for (int i = 0; i < 4; ++i) f[v].v[i] = fma2(mul2(add2(f[v].v[i], mean), inv), k.a[v].v[i], cb.v[i]);
+        if (live && c.on[v]) store_vec(h_out + c.col[v], f[v]);
       }
     }
+    if (CLS != 0 && !barrier) __syncthreads();
+    rows.release(row);
   }
 }
 
 // du -> the gradient of the norm's input: inv (du - n mean(du n) - mean(du)),
 // the last term for a layer norm only.  n is the normalised row.
 template <int V>
-__device__ __forceinline__ void norm_back(float (&du)[V][kVec], const float (&n)[V][kVec], const bool (&on)[V], float inv,
-                                          int kind, float inv_d, RowSum& sum) {
+__device__ __forceinline__ void norm_back(Vec (&du)[V], const Vec (&n)[V], const Columns<V>& c, float inv, int kind, RowSum& sum) {
   if (kind == SVGEAR_NORM_NONE) return;
   float2 s = make_float2(0.f, 0.f);
 #pragma unroll
+  for (int v = 0; v < V; ++v) {
+    f2 q = pair(0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q = fma2(du[v].v[i], n[v].v[i], q);
+    const float2 h = halves(q);
+    s.x += c.on[v] ? h.x + h.y : 0.f;
+  }
+  if (kind == SVGEAR_NORM_LAYER) {
+    s.y = total(du, c);
+    s = sum(s);
+  } else {
+    s.x = sum(s.x);
+  }
+  const f2 c1 = pair(-s.x * c.inv_d), c0 = pair(-s.y * c.inv_d), k = pair(inv);
+#pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      s.x = fmaf(du[v][i], n[v][i], s.x);
-      s.y += du[v][i];
-    }
-  s = sum(s);
-  const float c1 = s.x * inv_d, c0 = kind == SVGEAR_NORM_LAYER ? s.y * inv_d : 0.f;
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) du[v][i] = on[v] ? inv * (du[v][i] - c0 - n[v][i] * c1) : 0.f;
+    for (int i = 0; i < 4; ++i) du[v].v[i] = mul2(k, add2(fma2(n[v].v[i], c1, c0), du[v].v[i]));
 }
 
-template <typename TX, typename TY, int V>
-__global__ void __launch_bounds__(V == 1 ? 640 : 512) k_block_norm_back(const NormArgs p) {
+template <typename TX, typename TY, int CLS>
+__global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kThreads / Class<CLS, true>::kMax))
+    k_block_norm_back(const __grid_constant__ NormArgs p) {
+  constexpr int V = Class<CLS, true>::kV;
   __shared__ float2 scratch[64];
-  RowSum sum{scratch, p.tpr, 0};
-  const int slot = threadIdx.x / p.tpr, lane = threadIdx.x - slot * p.tpr;
-  const long long worker = (long long)blockIdx.x * (blockDim.x / p.tpr) + slot;
-  const float d = (float)p.D;
-  long long row = worker * p.chunk;
-  const long long end = row + p.chunk < p.N ? row + p.chunk : p.N;
-  const TX *x = static_cast<const TX*>(p.x), *dr = static_cast<const TX*>(p.dr);
-  const TY *y = static_cast<const TY*>(p.y), *dh = static_cast<const TY*>(p.dh);
-  int col[V];
-  bool on[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    col[v] = (v * p.tpr + lane) * kVec;
-    on[v] = col[v] < p.D;
-  }
-  int g = row < end ? group_of(p, (int)row) : p.G;
-  long long gend = row;
-  bool first = true;
-  float ca[V][kVec], cg[V][kVec];
-  float s1[V][kVec], s2[V][kVec], su[V][kVec];
-  Raw<TX> xr[V], rr[V];
-  Raw<TY> yr[V], hr[V];
-  auto fetch = [&](long long rw) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const bool ok = on[v] && rw < end;
-      const long long at = rw * p.D + col[v];
-      zero_raw(xr[v]); zero_raw(yr[v]); zero_raw(rr[v]); zero_raw(hr[v]);
-      if (ok) load_raw(xr[v], x + at);
-      if (ok && y) load_raw(yr[v], y + at);
-      if (ok && dr) load_raw(rr[v], dr + at);
-      if (ok && dh) load_raw(hr[v], dh + at);
-    }
-  };
+  RowSum sum(scratch, p.tpr);
+  const Place pl = place(p);
+  Columns<V> c;
+  c.init(p.D, p.tpr, pl.lane, sum);
+  typename std::conditional<CLS == 0, Direct<TX, TY, 4, V>, Ring<TX, TY, 4, V>>::type rows(p, c, pl.row, pl.end);
+  int g = pl.row < pl.end ? group_of(p, (int)pl.row) : 0;
+  long long gend = pl.row;
+  const bool barrier = (p.y && p.post != SVGEAR_NORM_NONE) || (p.dh && p.pre != SVGEAR_NORM_NONE);
+  const f2 a = pair(p.y ? p.a : 1.f);
+  Coefficients<V, CLS != 0> k(p, c, coefficient_memory(p));
+  Vec s1[V], s2[V], su[V];
+  TX* dx_out = static_cast<TX*>(p.dx) + pl.row * p.D;
+  TY* dy_out = static_cast<TY*>(p.dy) + pl.row * p.D;
   auto flush = [&]() {
-    float* part = p.part + (size_t)(worker + g) * 3 * p.D;
+    float* part = p.part + (size_t)(pl.worker + g) * 3 * p.D;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (on[v]) {
-        store_vec(part + col[v], s1[v]);
-        store_vec(part + p.D + col[v], s2[v]);
-        store_vec(part + 2 * (size_t)p.D + col[v], su[v]);
+      if (c.on[v]) {
+        store_vec(part + c.col[v], s1[v]);
+        store_vec(part + p.D + c.col[v], s2[v]);
+        store_vec(part + 2 * p.D + c.col[v], su[v]);
       }
   };
-  fetch(row);
-  for (int it = 0; it < p.chunk; ++it, ++row) {
-    if (g < p.G && row < end && (first || row >= gend)) {
-      if (!first) flush();
-      while (g < p.G && (gend = group_end(p, g)) <= row) ++g;
-      first = false;
-      if (g < p.G) {
+  for (int it = 0; it < p.chunk; ++it, dx_out += p.D, dy_out += p.D) {
+    const long long row = pl.row + it;
+    const bool live = row < pl.end;
+    if (p.tpr >= 32 && !live) break;
+    if (live && row >= gend) {
+      if (it) flush();
+      while ((gend = group_end(p, g)) <= row && g + 1 < p.G) ++g;
+      load_coefficients(p, g, c, k, false);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float w[kVec];
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) { ca[v][i] = cg[v][i] = 1.f; s1[v][i] = s2[v][i] = su[v][i] = 0.f; }
-          if (!on[v]) continue;
-          const size_t at = (size_t)g * p.D + col[v];
-          if (p.scale) {
-            load_f8(w, p.scale + at);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) ca[v][i] += w[i];
-          }
-          if (p.weight) {
-            load_f8(w, p.weight + col[v]);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) ca[v][i] *= w[i];
-          }
-          if (p.gate) load_f8(cg[v], p.gate + at);
-          if (p.post_weight) {
-            load_f8(w, p.post_weight + col[v]);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) cg[v][i] *= w[i];
-          }
-        }
+      for (int v = 0; v < V; ++v) {
+        fill(s1[v], 0.f);
+        fill(s2[v], 0.f);
+        fill(su[v], 0.f);
       }
     }
-    const bool live = g < p.G && row < end;
-    if (p.tpr >= 32 && !live) break;
-    float n[V][kVec], m[V][kVec], R[V][kVec];
+    Row<TX, TY, V> in;
+    rows.take(row, in);
+    Vec n[V], m[V], R[V];
     float inv_m = 1.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      unpack(xr[v], n[v]);
-      unpack(yr[v], m[v]);
-      unpack(hr[v], R[v]);
+      unpack(in.x[v], n[v]);
+      unpack(in.dh[v], R[v]);
     }
-    Raw<TX> rc[V];
+    if (p.y) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) rc[v] = rr[v];
-    fetch(row + 1);
-    if (y) {
-      inv_m = normalise<V>(m, on, p.post, d, p.eps, sum);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) n[v][i] = on[v] ? fmaf(p.a, n[v][i], cg[v][i] * m[v][i]) : 0.f;
-    }
-    if (dh) {
-      const float inv_n = normalise<V>(n, on, p.pre, d, p.eps, sum);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          if (live) {
-            s1[v][i] += R[v][i];
-            s2[v][i] = fmaf(R[v][i], n[v][i], s2[v][i]);
-          }
-          R[v][i] = on[v] ? R[v][i] * ca[v][i] : 0.f;
-        }
-      norm_back<V>(R, n, on, inv_n, p.pre, 1.f / d, sum);
-    }
-    if (dr) {
+      for (int v = 0; v < V; ++v) unpack(in.y[v], m[v]);
+      inv_m = normalise<V>(m, c, p.post, p.eps, sum);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        unpack(rc[v], n[v]);
+        const Vec cg = k.get_g(v);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) R[v][i] += n[v][i];
+        for (int i = 0; i < 4; ++i) n[v].v[i] = fma2(a, n[v].v[i], mul2(cg.v[i], m[v].v[i]));
       }
     }
-    const float a = y ? p.a : 1.f;
+    if (p.dh) {
+      const float inv_n = normalise<V>(n, c, p.pre, p.eps, sum);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (CLS != 0 || live) {
+            s1[v].v[i] = add2(s1[v].v[i], R[v].v[i]);
+            s2[v].v[i] = fma2(R[v].v[i], n[v].v[i], s2[v].v[i]);
+          }
+          R[v].v[i] = mul2(R[v].v[i], k.a[v].v[i]);
+        }
+      norm_back<V>(R, n, c, inv_n, p.pre, sum);
+    }
+    if (p.dr) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        unpack(in.dr[v], n[v]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) R[v].v[i] = add2(R[v].v[i], n[v].v[i]);
+      }
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) n[v][i] = a * R[v][i];
-      if (live && on[v]) store_vec(static_cast<TX*>(p.dx) + row * p.D + col[v], n[v]);
+      for (int i = 0; i < 4; ++i) n[v].v[i] = mul2(a, R[v].v[i]);
+      if (live && c.on[v]) store_vec(dx_out + c.col[v], n[v]);
     }
-    if (y) {
+    if (p.y) {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v) {
+        const Vec cg = k.get_g(v);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          if (live) su[v][i] = fmaf(R[v][i], m[v][i], su[v][i]);
-          R[v][i] = on[v] ? R[v][i] * cg[v][i] : 0.f;
+        for (int i = 0; i < 4; ++i) {
+          if (CLS != 0 || live) su[v].v[i] = fma2(R[v].v[i], m[v].v[i], su[v].v[i]);
+          R[v].v[i] = mul2(R[v].v[i], cg.v[i]);
         }
-      norm_back<V>(R, m, on, inv_m, p.post, 1.f / d, sum);
+      }
+      norm_back<V>(R, m, c, inv_m, p.post, sum);
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (live && on[v]) store_vec(static_cast<TY*>(p.dy) + row * p.D + col[v], R[v]);
+        if (live && c.on[v]) store_vec(dy_out + c.col[v], R[v]);
     }
+    if (CLS != 0 && !barrier) __syncthreads();
+    rows.release(row);
   }
-  // The last group this worker had rows of; when it left through the end of
-  // the last group, that group was flushed on the way.
-  if (!first && g < p.G) flush();
+  if (pl.row < pl.end) flush();
 }
 
 struct SumArgs {
@@ -384,7 +587,7 @@ constexpr int kSumLanes = 16;
 
 // Column sums of one group: 32 columns per block, the group's slots dealt to
 // 16 warps, their results added in warp order.
-__global__ void __launch_bounds__(32 * kSumLanes) k_group_sums(const NormArgs p, const SumArgs q) {
+__global__ void __launch_bounds__(32 * kSumLanes) k_group_sums(const __grid_constant__ NormArgs p, const __grid_constant__ SumArgs q) {
   __shared__ float red[3][kSumLanes][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
@@ -423,7 +626,7 @@ __global__ void __launch_bounds__(32 * kSumLanes) k_group_sums(const NormArgs p,
 }
 
 // Gradients of the affine weights: the groups' sums weighted by 1 + s or g.
-__global__ void __launch_bounds__(32 * kSumLanes) k_weight_sums(const NormArgs p, const SumArgs q) {
+__global__ void __launch_bounds__(32 * kSumLanes) k_weight_sums(const __grid_constant__ NormArgs p, const __grid_constant__ SumArgs q) {
   __shared__ float red[3][kSumLanes][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
@@ -453,32 +656,47 @@ __global__ void __launch_bounds__(32 * kSumLanes) k_weight_sums(const NormArgs p
   }
 }
 
-// Launch shape: threads per row, vectors per thread, rows per worker.
+// Launch shape: block class, threads per row, rows per worker, ring stages.
 struct Shape {
-  int V, tpr, block, chunk, grid;
+  int cls, tpr, block, chunk, grid, stages, ring_bytes, smem;
   long long workers;
 };
 
-Shape norm_shape(int N, int D, bool back) {
+constexpr int kSmemPerSm = 228 * 1024, kSmemPerBlock = 2048;  // 1 KB per block is the system's, the rest static arrays
+
+Shape norm_shape(const svgear_norm_params* p, bool back) {
   Shape s;
-  const int nvec = D / kVec;
-  s.V = nvec > 640 ? 2 : 1;
+  const int nvec = p->D / kVec, N = p->N;
+  int threads;  // resident per SM
   if (nvec <= 32) {
+    s.cls = 0;
     s.tpr = nvec <= 8 ? 8 : nvec <= 16 ? 16 : 32;
     s.block = 128;
+    threads = back ? Class<0, true>::kThreads : Class<0, false>::kThreads;
   } else {
-    s.tpr = ((nvec + s.V - 1) / s.V + 31) / 32 * 32;
-    s.block = s.tpr;
+    s.tpr = s.block = std::max(64, (nvec + 63) / 64 * 32);
+    s.cls = s.block <= 128 ? 1 : s.block <= 320 ? 2 : 3;
+    threads = s.cls == 1   ? (back ? Class<1, true>::kThreads : Class<1, false>::kThreads)
+              : s.cls == 2 ? (back ? Class<2, true>::kThreads : Class<2, false>::kThreads)
+                           : Class<3, true>::kThreads;
   }
   const int per = s.block / s.tpr;
-  // Workers beyond what the SMs hold at once only add partial sums; the
-  // backward pass of narrow rows is held to 2,048 of them for the same reason.
-  const int ctas = back ? std::max(1, std::min(1024 / s.block, 8)) : std::max(1, std::min(2048 / s.block, 16));
-  long long want = std::min<long long>(N, 148LL * ctas * per);
-  if (back && nvec <= 32) want = std::min<long long>(want, 2048);
+  const int stage = p->D * ((p->res_dtype == DT_F32 ? 4 : 2) + (p->dtype == DT_F32 ? 4 : 2)) * (back ? 2 : 1);
+  const int coefs = 2 * p->D * (int)sizeof(float);
+  // Blocks per SM: what the registers allow, as long as each has two stages.
+  int blocks = std::max(1, std::min(threads / s.block, 8));
+  auto stages = [&]() { return (kSmemPerSm / blocks - kSmemPerBlock - coefs) / stage; };
+  while (s.cls != 0 && blocks > 1 && stages() < 2) --blocks;
+  // As many workers as the SMs hold at once; more would only add partial sums.
+  // The backward pass of narrow rows is held to 2,048 for the same reason.
+  long long want = std::min<long long>(N, 148LL * blocks * per);
+  if (back && s.cls == 0) want = std::min<long long>(want, 2048);
   s.chunk = (int)((N + want - 1) / want);
   s.workers = (N + s.chunk - 1) / s.chunk;
   s.grid = (int)((s.workers + per - 1) / per);
+  s.stages = s.cls == 0 ? 0 : std::max(1, std::min({stages(), kMaxStages, s.chunk}));
+  s.ring_bytes = s.stages * stage;
+  s.smem = s.cls == 0 ? 0 : s.ring_bytes + coefs;
   return s;
 }
 
@@ -489,34 +707,44 @@ NormArgs norm_args(const BlockNorm& b, const Shape& s) {
   p.post_weight = b.post_weight;
   p.offsets = b.offsets;
   p.N = b.p->N; p.D = b.p->D; p.G = b.p->G; p.pre = b.p->pre; p.post = b.p->post;
-  p.tpr = s.tpr; p.chunk = s.chunk;
+  p.tpr = s.tpr; p.chunk = s.chunk; p.stages = s.stages; p.ring_bytes = s.ring_bytes;
   p.eps = b.p->eps; p.a = b.p->res_scale;
   p.r = b.r; p.h = b.h; p.dx = b.dx; p.dy = b.dy;
+  p.status = status_word();
   return p;
 }
 
-template <typename TX, typename TY>
-void launch_norm(const NormArgs& p, const Shape& s, bool back, cudaStream_t st) {
-  if (back) {
-    if (s.V == 1) k_block_norm_back<TX, TY, 1><<<s.grid, s.block, 0, st>>>(p);
-    else k_block_norm_back<TX, TY, 2><<<s.grid, s.block, 0, st>>>(p);
-  } else {
-    if (s.V == 1) k_block_norm<TX, TY, 1><<<s.grid, s.block, 0, st>>>(p);
-    else k_block_norm<TX, TY, 2><<<s.grid, s.block, 0, st>>>(p);
+template <typename TX, typename TY, int CLS>
+cudaError_t launch_class(const NormArgs& p, const Shape& s, bool back, cudaStream_t st) {
+  const auto kernel = back ? k_block_norm_back<TX, TY, CLS> : k_block_norm<TX, TY, CLS>;
+  if (s.smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem);
+    if (e != cudaSuccess) return e;
   }
+  kernel<<<s.grid, s.block, s.smem, st>>>(p);
   note_launch();
+  return cudaGetLastError();
 }
 
-void launch_typed(const BlockNorm& b, const NormArgs& p, const Shape& s, bool back, cudaStream_t st) {
-  if (b.p->dtype == DT_F32) launch_norm<float, float>(p, s, back, st);
-  else if (b.p->res_dtype == DT_F32) launch_norm<float, bf16>(p, s, back, st);
-  else launch_norm<bf16, bf16>(p, s, back, st);
+template <typename TX, typename TY>
+cudaError_t launch_norm(const NormArgs& p, const Shape& s, bool back, cudaStream_t st) {
+  if (s.cls == 0) return launch_class<TX, TY, 0>(p, s, back, st);
+  if (s.cls == 1) return launch_class<TX, TY, 1>(p, s, back, st);
+  if (s.cls == 2) return launch_class<TX, TY, 2>(p, s, back, st);
+  return launch_class<TX, TY, 3>(p, s, back, st);
+}
+
+cudaError_t launch_typed(const BlockNorm& b, const NormArgs& p, const Shape& s, bool back, cudaStream_t st) {
+  if (!p.status) return cudaErrorInvalidValue;
+  if (b.p->dtype == DT_F32) return launch_norm<float, float>(p, s, back, st);
+  if (b.p->res_dtype == DT_F32) return launch_norm<float, bf16>(p, s, back, st);
+  return launch_norm<bf16, bf16>(p, s, back, st);
 }
 
 }  // namespace
 
 size_t block_norm_back_ws_bytes(const svgear_norm_params* p) {
-  const Shape s = norm_shape(p->N, p->D, true);
+  const Shape s = norm_shape(p, true);
   Carve cv(nullptr);
   cv.take<float>((size_t)(s.workers + p->G) * 3 * p->D);
   cv.take<float>((size_t)p->G * 3 * p->D);
@@ -524,13 +752,12 @@ size_t block_norm_back_ws_bytes(const svgear_norm_params* p) {
 }
 
 cudaError_t block_norm_run(const BlockNorm& b, cudaStream_t st) {
-  const Shape s = norm_shape(b.p->N, b.p->D, false);
-  launch_typed(b, norm_args(b, s), s, false, st);
-  return cudaGetLastError();
+  const Shape s = norm_shape(b.p, false);
+  return launch_typed(b, norm_args(b, s), s, false, st);
 }
 
 cudaError_t block_norm_back_run(const BlockNorm& b, void* ws, cudaStream_t st) {
-  const Shape s = norm_shape(b.p->N, b.p->D, true);
+  const Shape s = norm_shape(b.p, true);
   NormArgs p = norm_args(b, s);
   Carve cv(ws);
   p.part = cv.take<float>((size_t)(s.workers + p.G) * 3 * p.D);
@@ -539,8 +766,7 @@ cudaError_t block_norm_back_run(const BlockNorm& b, void* ws, cudaStream_t st) {
   q.dgate = b.dgate; q.dscale = b.dscale; q.dshift = b.dshift;
   q.dweight = b.dweight; q.dbias = b.dbias; q.dpost_weight = b.dpost_weight;
   if (q.dweight || q.dbias || q.dpost_weight) q.sums = cv.take<float>((size_t)p.G * 3 * p.D);
-  launch_typed(b, p, s, true, st);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_typed(b, p, s, true, st);
   const int cols = (p.D + 31) / 32;
   if (e == cudaSuccess && (q.dgate || q.dscale || q.dshift || q.sums)) {
     k_group_sums<<<dim3(cols, std::min(p.G, 32768)), 32 * kSumLanes, 0, st>>>(p, q);

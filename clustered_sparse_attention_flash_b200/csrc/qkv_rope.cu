@@ -135,37 +135,65 @@ __device__ __forceinline__ void read_angles(const float2* cs, int j, int d, floa
   for (int i = 0; i < kVec; ++i) c[i] = HALF ? cs[j * 8 + i] : i < 4 ? cs[j * 4 + i] : cs[d / 4 + j * 4 + i - 4];
 }
 
-template <typename T, bool HALF>
-__global__ void __launch_bounds__(1024) k_qkv_rope(const __grid_constant__ RopeArgs p) {
+// Block classes: most threads of a block, and the blocks an SM is to hold (the
+// launch bounds set the registers, the grid counts on them).
+template <int MAXT, bool BACK>
+struct Class {
+  static constexpr int kThreads = MAXT == 128 ? (BACK ? 384 : 512) : MAXT == 384 ? (BACK ? 384 : 768) : 1024;  // per SM
+  static constexpr int kBlocks = kThreads / MAXT;
+};
+
+template <typename T, bool HALF, int MAXT>
+__global__ void __launch_bounds__(MAXT, (Class<MAXT, false>::kBlocks)) k_qkv_rope(const __grid_constant__ RopeArgs p) {
   __shared__ float2 scratch[64];
-  __shared__ float2 table[2][32][kMaxPairs];
-  RowSum sum{scratch, p.tpt, 0};
+  __shared__ float2 table[2][MAXT == 128 ? 32 : 1][kMaxPairs];
+  constexpr bool kAhead = sizeof(T) == 2 && MAXT < 1024;  // the next token is loaded while this one is computed
+  RowSum sum(scratch, p.tpt);
   const Place pl = place(p);
-  const int half = p.d / 2;
+  const int half = p.d / 2, head = pl.off / p.d;
   const float inv_c = 1.f / (float)(p.norm == SVGEAR_QKNORM_TOKEN ? p.H * p.d : p.d);
+  Raw<T> next[3][2];
+  auto fetch = [&](long long t, Raw<T>(&raw)[3][2]) {
+    const int b = (int)(t / p.N), n = (int)(t - (long long)b * p.N);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      zero_raw(raw[k][0]);
+      zero_raw(raw[k][1]);
+      if (p.in[k] && t < pl.end && pl.on) {
+        const T* x = static_cast<const T*>(p.in[k]) + b * p.batch[k] + n * p.ld[k] + pl.off;
+        load_raw(raw[k][0], x);
+        load_raw(raw[k][1], x + half);
+      }
+    }
+  };
+  if (kAhead) fetch(pl.t, next);
   for (int it = 0; it < p.chunk; ++it) {
     const long long t = pl.t + it;
     const bool live = t < pl.end;
     if (p.tpt >= 32 && !live) break;  // uniform over the worker
     const int b = live ? (int)(t / p.N) : 0, n = live ? (int)(t - (long long)b * p.N) : 0;
     float2* cs = table[it & 1][pl.slot];
+    const long long o = ((long long)(b * p.H + head) * p.out_tokens + n) * p.d + pl.j * kVec;
     Raw<T> raw[3][2];
+    if (kAhead) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      zero_raw(raw[k][0]);
-      zero_raw(raw[k][1]);
-      if (p.in[k] && live && pl.on) {
-        const T* x = static_cast<const T*>(p.in[k]) + b * p.batch[k] + n * p.ld[k] + pl.off;
-        load_raw(raw[k][0], x);
-        load_raw(raw[k][1], x + half);
+      for (int k = 0; k < 3; ++k) {
+        raw[k][0] = next[k][0];
+        raw[k][1] = next[k][1];
       }
+    } else {
+      fetch(t, raw);
     }
+    if (p.in[2] && live && pl.on) {
+      T* out = static_cast<T*>(p.out[2]) + o;
+      store_raw(out, raw[2][0]);
+      store_raw(out + half, raw[2][1]);
+    }
+    if (kAhead) fetch(t + 1, next);
     token_table(p, b, n, cs, pl.lane, p.tpt);
     if (p.tpt > 32) __syncthreads(); else __syncwarp();
     float2 c[kVec];
     read_angles<HALF>(cs, pl.j, p.d, c);
-    const int head = pl.off / p.d;
-    const long long o = ((long long)(b * p.H + head) * p.out_tokens + n) * p.d + pl.j * kVec;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (!p.in[k]) continue;
@@ -196,57 +224,70 @@ __global__ void __launch_bounds__(1024) k_qkv_rope(const __grid_constant__ RopeA
         store_vec(out + half, hi);
       }
     }
-    if (p.in[2] && live && pl.on) {
-      T* out = static_cast<T*>(p.out[2]) + o;
-      store_raw(out, raw[2][0]);
-      store_raw(out + half, raw[2][1]);
-    }
   }
 }
 
-template <typename T, bool HALF>
-__global__ void __launch_bounds__(1024) k_qkv_rope_back(const __grid_constant__ RopeArgs p) {
+template <typename T, bool HALF, int MAXT>
+__global__ void __launch_bounds__(MAXT, (Class<MAXT, true>::kBlocks)) k_qkv_rope_back(const __grid_constant__ RopeArgs p) {
   __shared__ float2 scratch[64];
-  __shared__ float2 table[2][32][kMaxPairs];
-  RowSum sum{scratch, p.tpt, 0};
+  constexpr int kTable = 2 * (MAXT == 128 ? 32 : 1) * kMaxPairs;
+  constexpr int kRed = MAXT / 32 * kMaxPairs;  // [warps][2 * kMaxPairs] floats, in the table's place at the end
+  __shared__ float2 store[kTable > kRed ? kTable : kRed];
+  constexpr bool kAhead = sizeof(T) == 2 && MAXT < 1024;
+  RowSum sum(scratch, p.tpt);
   const Place pl = place(p);
-  const int half = p.d / 2;
+  const int half = p.d / 2, head = pl.off / p.d;
   const float inv_c = 1.f / (float)(p.norm == SVGEAR_QKNORM_TOKEN ? p.H * p.d : p.d);
   float dw[2][2][kVec];
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int i = 0; i < kVec; ++i) dw[k][0][i] = dw[k][1][i] = 0.f;
+  Raw<T> next[5][2];  // dQ, dK, dV, q, k
+  auto fetch = [&](long long t, Raw<T>(&raw)[5][2]) {
+    const int b = (int)(t / p.N), n = (int)(t - (long long)b * p.N);
+    const bool ok = t < pl.end && pl.on;
+    const long long o = ((long long)(b * p.H + head) * p.out_tokens + n) * p.d + pl.j * kVec;
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+      zero_raw(raw[k][0]);
+      zero_raw(raw[k][1]);
+      const T* x;
+      if (k < 3) {
+        if (!ok || !p.grad[k]) continue;
+        x = static_cast<const T*>(p.grad[k]) + o;
+      } else {
+        if (!ok || p.norm == SVGEAR_QKNORM_NONE || !p.grad[k - 3]) continue;
+        x = static_cast<const T*>(p.in[k - 3]) + b * p.batch[k - 3] + n * p.ld[k - 3] + pl.off;
+      }
+      load_raw(raw[k][0], x);
+      load_raw(raw[k][1], x + half);
+    }
+  };
+  if (kAhead) fetch(pl.t, next);
   for (int it = 0; it < p.chunk; ++it) {
     const long long t = pl.t + it;
     const bool live = t < pl.end;
     if (p.tpt >= 32 && !live) break;
     const int b = live ? (int)(t / p.N) : 0, n = live ? (int)(t - (long long)b * p.N) : 0;
-    const int head = pl.off / p.d;
-    const long long o = ((long long)(b * p.H + head) * p.out_tokens + n) * p.d + pl.j * kVec;
     const long long go = b * p.out_batch + n * p.out_ld + pl.off;
-    float2* cs = table[it & 1][pl.slot];
-    Raw<T> raw[2][2], gr[3][2];
+    float2* cs = store + ((it & 1) * (MAXT == 128 ? 32 : 1) + pl.slot) * kMaxPairs;
+    Raw<T> raw[5][2];
+    if (kAhead) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      zero_raw(gr[k][0]);
-      zero_raw(gr[k][1]);
-      if (p.grad[k] && live && pl.on) {
-        const T* x = static_cast<const T*>(p.grad[k]) + o;
-        load_raw(gr[k][0], x);
-        load_raw(gr[k][1], x + half);
+      for (int k = 0; k < 5; ++k) {
+        raw[k][0] = next[k][0];
+        raw[k][1] = next[k][1];
       }
+    } else {
+      fetch(t, raw);
     }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      zero_raw(raw[k][0]);
-      zero_raw(raw[k][1]);
-      if (p.norm != SVGEAR_QKNORM_NONE && p.grad[k] && live && pl.on) {
-        const T* x = static_cast<const T*>(p.in[k]) + b * p.batch[k] + n * p.ld[k] + pl.off;
-        load_raw(raw[k][0], x);
-        load_raw(raw[k][1], x + half);
-      }
+    if (p.grad[2] && live && pl.on) {
+      T* out = static_cast<T*>(p.out[2]) + go;
+      store_raw(out, raw[2][0]);
+      store_raw(out + half, raw[2][1]);
     }
+    if (kAhead) fetch(t + 1, next);
     token_table(p, b, n, cs, pl.lane, p.tpt);
     if (p.tpt > 32) __syncthreads(); else __syncwarp();
     float2 c[kVec];
@@ -255,13 +296,13 @@ __global__ void __launch_bounds__(1024) k_qkv_rope_back(const __grid_constant__ 
     for (int k = 0; k < 2; ++k) {
       if (!p.grad[k]) continue;
       float lo[kVec], hi[kVec];
-      unpack(gr[k][0], lo);
-      unpack(gr[k][1], hi);
+      unpack(raw[k][0], lo);
+      unpack(raw[k][1], hi);
       turn16<HALF>(lo, hi, c, -1.f);
       if (p.norm != SVGEAR_QKNORM_NONE) {
         float nl[kVec], nh[kVec];
-        unpack(raw[k][0], nl);
-        unpack(raw[k][1], nh);
+        unpack(raw[3 + k][0], nl);
+        unpack(raw[3 + k][1], nh);
         const float inv = rsqrtf(norm_sum(dot16(nl, nl, nh, nh), p.norm, pl.lanes, sum) * inv_c + p.eps);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
@@ -293,11 +334,6 @@ __global__ void __launch_bounds__(1024) k_qkv_rope_back(const __grid_constant__ 
         store_vec(out, lo);
         store_vec(out + half, hi);
       }
-    }
-    if (p.grad[2] && live && pl.on) {
-      T* out = static_cast<T*>(p.out[2]) + go;
-      store_raw(out, gr[2][0]);
-      store_raw(out + half, gr[2][1]);
     }
   }
   if (!p.part) return;
@@ -332,7 +368,7 @@ __global__ void __launch_bounds__(1024) k_qkv_rope_back(const __grid_constant__ 
       }
     return;
   }
-  float(*wred)[2 * kMaxPairs] = reinterpret_cast<float(*)[2 * kMaxPairs]>(&table[0][0][0]);  // [32][128], in the table's place
+  float(*wred)[2 * kMaxPairs] = reinterpret_cast<float(*)[2 * kMaxPairs]>(store);
   for (int k = 0; k < 2; ++k) {
     __syncthreads();
     if ((threadIdx.x & 31) < pl.lanes)
@@ -374,7 +410,7 @@ __global__ void __launch_bounds__(32 * kSumLanes) k_rope_weight_sums(const float
 }
 
 struct Shape {
-  int tpt, block, chunk, grid;
+  int tpt, block, cls, chunk, grid;
   long long workers;
 };
 
@@ -387,10 +423,14 @@ Shape rope_shape(const svgear_rope_params* p, bool back) {
   } else {
     s.tpt = s.block = (items + 31) / 32 * 32;
   }
+  s.cls = s.block <= 128 ? 128 : s.block <= 384 ? 384 : 1024;
   const int per = s.block / s.tpt;
   const long long tokens = (long long)p->B * p->N;
-  const int ctas = std::max(1, std::min((back ? 1024 : 1536) / s.block, 8));
-  long long want = std::min(tokens, 148LL * ctas * per);
+  // As many blocks as the SMs hold at once, each with a run of tokens.
+  const int threads = s.cls == 1024 ? 1024
+                      : s.cls == 384 ? (back ? Class<384, true>::kThreads : Class<384, false>::kThreads)
+                                     : (back ? Class<128, true>::kThreads : Class<128, false>::kThreads);
+  long long want = std::min(tokens, 148LL * (threads / s.block) * per);
   if (back) want = std::min(want, 4096LL);
   s.chunk = (int)((tokens + want - 1) / want);
   s.workers = (tokens + s.chunk - 1) / s.chunk;
@@ -433,16 +473,24 @@ RopeArgs rope_args(const svgear_rope_params* p, const float* wq, const float* wk
   return a;
 }
 
+template <typename T, bool HALF, int MAXT>
+void launch_class(const RopeArgs& a, const Shape& s, bool back, cudaStream_t st) {
+  if (back) k_qkv_rope_back<T, HALF, MAXT><<<s.grid, s.block, 0, st>>>(a);
+  else k_qkv_rope<T, HALF, MAXT><<<s.grid, s.block, 0, st>>>(a);
+  note_launch();
+}
+
+template <typename T, bool HALF>
+void launch_half(const RopeArgs& a, const Shape& s, bool back, cudaStream_t st) {
+  if (s.cls == 128) launch_class<T, HALF, 128>(a, s, back, st);
+  else if (s.cls == 384) launch_class<T, HALF, 384>(a, s, back, st);
+  else launch_class<T, HALF, 1024>(a, s, back, st);
+}
+
 template <typename T>
 void launch_rope(const RopeArgs& a, const Shape& s, bool half, bool back, cudaStream_t st) {
-  if (back) {
-    if (half) k_qkv_rope_back<T, true><<<s.grid, s.block, 0, st>>>(a);
-    else k_qkv_rope_back<T, false><<<s.grid, s.block, 0, st>>>(a);
-  } else {
-    if (half) k_qkv_rope<T, true><<<s.grid, s.block, 0, st>>>(a);
-    else k_qkv_rope<T, false><<<s.grid, s.block, 0, st>>>(a);
-  }
-  note_launch();
+  if (half) launch_half<T, true>(a, s, back, st);
+  else launch_half<T, false>(a, s, back, st);
 }
 
 }  // namespace

@@ -62,6 +62,78 @@ __device__ __forceinline__ void load_f8(float (&f)[kVec], const float* p) {
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
+// Two floats in one register pair: the packed float32 instructions of sm_100
+// do twice the work per issue slot.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ f2 pair(float x) { return pair(x, x); }
+__device__ __forceinline__ float2 halves(f2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// A vector as four pairs.
+struct Vec {
+  f2 v[4];
+};
+__device__ __forceinline__ void unpack(const Raw<bf16>& r, Vec& f) {
+  const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack(const Raw<float>& r, Vec& f) {
+  f.v[0] = pair(r.a.x, r.a.y);
+  f.v[1] = pair(r.a.z, r.a.w);
+  f.v[2] = pair(r.b.x, r.b.y);
+  f.v[3] = pair(r.b.z, r.b.w);
+}
+__device__ __forceinline__ void store_vec(bf16* p, const Vec& f) {
+  uint4 u;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 h = halves(f.v[i]);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(h.x, h.y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p) = u;
+}
+__device__ __forceinline__ void store_vec(float* p, const Vec& f) {
+  const float2 a = halves(f.v[0]), b = halves(f.v[1]), c = halves(f.v[2]), d = halves(f.v[3]);
+  reinterpret_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
+}
+__device__ __forceinline__ void load_vec(Vec& f, const float* p) {
+  Raw<float> r;
+  r.a = reinterpret_cast<const float4*>(p)[0];
+  r.b = reinterpret_cast<const float4*>(p)[1];
+  unpack(r, f);
+}
+__device__ __forceinline__ void fill(Vec& f, float x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.v[i] = pair(x);
+}
+
 // Sums over the `width` lanes of a worker: 4, 8, 16 or 32 lanes of a warp, or a
 // whole block of up to 32 warps.  Every thread of the block calls it the same
 // number of times; `scratch` ([2][32]) alternates between two halves, so one
@@ -69,28 +141,50 @@ __device__ __forceinline__ void load_f8(float (&f)[kVec], const float* p) {
 // sum's barrier, which every reader of it has reached.
 struct RowSum {
   float2* scratch;
-  int width, phase;
-  __device__ __forceinline__ float2 operator()(float2 v) {
+  int width, phase, top, mask;  // top, mask: the tree over the warps' totals
+  __device__ __forceinline__ RowSum(float2* s, int w) : scratch(s), width(w), phase(0), top(0), mask(0) {
+    if (w > 32) {
+      for (top = 1; top < w >> 5; top <<= 1) {}
+      mask = top - 1;
+      top >>= 1;
+    }
+  }
+  __device__ __forceinline__ float2 lanes(float2 v) const {
     for (int o = (width < 32 ? width : 32) >> 1; o > 0; o >>= 1) {
       v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
       v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
     }
+    return v;
+  }
+  __device__ __forceinline__ float lanes(float v) const {
+    for (int o = (width < 32 ? width : 32) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  // Trades the warps' values: lane i gets warp (i & mask)'s, zeros behind the last warp.
+  __device__ __forceinline__ float2 trade(float2 v) {
+    float2* s = scratch + phase * 32;
+    phase ^= 1;
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int i = threadIdx.x & mask;
+    return i < width >> 5 ? s[i] : make_float2(0.f, 0.f);
+  }
+  __device__ __forceinline__ float warps(float v) const {
+    for (int o = top; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  __device__ __forceinline__ float2 operator()(float2 v) {
+    v = lanes(v);
     if (width > 32) {
-      float2* s = scratch + phase * 32;
-      phase ^= 1;
-      if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-      __syncthreads();
-      const int nw = width >> 5, lane = threadIdx.x & 31;
-      v = lane < nw ? s[lane] : make_float2(0.f, 0.f);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-      }
+      v = trade(v);
+      v = make_float2(warps(v.x), warps(v.y));
     }
     return v;
   }
-  __device__ __forceinline__ float operator()(float v) { return (*this)(make_float2(v, 0.f)).x; }
+  __device__ __forceinline__ float operator()(float v) {
+    v = lanes(v);
+    return width > 32 ? warps(trade(make_float2(v, 0.f)).x) : v;
+  }
 };
 
 }  // namespace svg

@@ -16,10 +16,12 @@
 // thread: adjacent pairs inside each vector, half-split pairs across the two.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
 #include "rowvec.cuh"
+#include "tc_common.cuh"
 
 namespace svg {
 
@@ -36,352 +38,645 @@ struct RopeArgs {
   const int32_t* pos;
   long long pos_batch;  // int32 per batch entry (0: shared)
   float* part;          // backward: [workers][2][C] partial weight gradients
-  int B, N, H, d, out_tokens, norm, tpt, chunk;
+  int B, N, H, d, out_tokens, norm, tpt, chunk, stages, ring_bytes, weight_bytes, table_tokens, grads_at;
   int pairs0, pairs01, pairs;  // pairs of axis 0, of axes 0-1, of all axes
   int g1, g2, vol;             // grid extents of axes 1 and 2, grid tokens
   int origin[3];
   float eps;
+  int* status;
   double freq[kMaxPairs];  // turns per position
 };
 
-// cos/sin of one token's pairs; identity where nothing turns.
-__device__ __forceinline__ void token_table(const RopeArgs& p, int b, int n, float2* cs, int lane, int width) {
-  for (int i = lane; i < p.d / 2; i += width) {
-    float2 v = make_float2(1.f, 0.f);
-    if (i < p.pairs) {
-      const int ax = i < p.pairs0 ? 0 : i < p.pairs01 ? 1 : 2;
-      int x = 0;
-      bool turn = true;
-      if (p.pos) {
-        x = p.pos[(long long)b * p.pos_batch + (long long)n * 3 + ax];
-      } else if (n < p.vol) {
-        x = ax == 2 ? n % p.g2 : ax == 1 ? n / p.g2 % p.g1 : n / p.g2 / p.g1;
-      } else {
-        turn = false;
-      }
-      if (turn) {
-        double t = ((double)x + p.origin[ax]) * p.freq[i];
-        t -= rint(t);
-        sincospif(2.f * (float)t, &v.y, &v.x);
-      }
+// cos and sin of pair i of token (b, n); the identity where nothing turns.
+__device__ __forceinline__ float2 cos_sin(const RopeArgs& p, int b, int n, int i) {
+  float2 v = make_float2(1.f, 0.f);
+  if (i < p.pairs) {
+    const int ax = i < p.pairs0 ? 0 : i < p.pairs01 ? 1 : 2;
+    int x = 0;
+    bool turn = true;
+    if (p.pos) {
+      x = p.pos[(long long)b * p.pos_batch + (long long)n * 3 + ax];
+    } else if (n < p.vol) {
+      x = ax == 2 ? n % p.g2 : ax == 1 ? n / p.g2 % p.g1 : n / p.g2 / p.g1;
+    } else {
+      turn = false;
     }
-    cs[i] = v;
-  }
-}
-
-// Turns the 16 elements of a thread by its 8 angles (sign -1: back).
-template <bool HALF>
-__device__ __forceinline__ void turn16(float (&lo)[kVec], float (&hi)[kVec], const float2 (&cs)[kVec], float sign) {
-  if (HALF) {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const float a = lo[i], b = hi[i], s = sign * cs[i].y;
-      lo[i] = a * cs[i].x - b * s;
-      hi[i] = a * s + b * cs[i].x;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float a = lo[2 * i], b = lo[2 * i + 1], s = sign * cs[i].y;
-      lo[2 * i] = a * cs[i].x - b * s;
-      lo[2 * i + 1] = a * s + b * cs[i].x;
-      a = hi[2 * i], b = hi[2 * i + 1], s = sign * cs[4 + i].y;
-      hi[2 * i] = a * cs[4 + i].x - b * s;
-      hi[2 * i + 1] = a * s + b * cs[4 + i].x;
+    if (turn) {
+      double t = ((double)x + p.origin[ax]) * p.freq[i];
+      t -= rint(t);
+      sincospif(2.f * (float)t, &v.y, &v.x);
     }
   }
-}
-
-__device__ __forceinline__ float dot16(const float (&a)[kVec], const float (&b)[kVec], const float (&c)[kVec],
-                                       const float (&d)[kVec]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) s = fmaf(a[i], b[i], fmaf(c[i], d[i], s));
-  return s;
-}
-
-// Sum over the threads of a head (d/16 lanes) or of the token.
-__device__ __forceinline__ float norm_sum(float v, int norm, int lanes, RowSum& sum) {
-  if (norm == SVGEAR_QKNORM_TOKEN) return sum(v);
-  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// What both kernels know about a thread: its worker, its place in a token.
-struct Place {
-  int slot, lane, lanes, j, off;  // off: element offset of the low vector in a token
-  bool on;
-  long long t, end;               // tokens [t, end) of this worker, b*N + n
+// A thread's 16 elements of a head as two sets of packed floats: A the first
+// and B the second members of its eight pairs, in the order of its angles.
+struct Sixteen {
+  f2 A[4], B[4];
 };
 
+__device__ __forceinline__ f2 low_bf16(uint32_t a, uint32_t b) { return pair(__uint_as_float(a << 16), __uint_as_float(b << 16)); }
+__device__ __forceinline__ f2 high_bf16(uint32_t a, uint32_t b) {
+  return pair(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u));
+}
+template <bool HALF>
+__device__ __forceinline__ void spread(const Raw<bf16>& lo, const Raw<bf16>& hi, Sixteen& z) {
+  if (HALF) {
+    Vec a, b;
+    unpack(lo, a);
+    unpack(hi, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { z.A[i] = a.v[i]; z.B[i] = b.v[i]; }
+  } else {
+    z.A[0] = low_bf16(lo.u.x, lo.u.y); z.B[0] = high_bf16(lo.u.x, lo.u.y);
+    z.A[1] = low_bf16(lo.u.z, lo.u.w); z.B[1] = high_bf16(lo.u.z, lo.u.w);
+    z.A[2] = low_bf16(hi.u.x, hi.u.y); z.B[2] = high_bf16(hi.u.x, hi.u.y);
+    z.A[3] = low_bf16(hi.u.z, hi.u.w); z.B[3] = high_bf16(hi.u.z, hi.u.w);
+  }
+}
+template <bool HALF>
+__device__ __forceinline__ void spread(const Raw<float>& lo, const Raw<float>& hi, Sixteen& z) {
+  if (HALF) {
+    Vec a, b;
+    unpack(lo, a);
+    unpack(hi, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { z.A[i] = a.v[i]; z.B[i] = b.v[i]; }
+  } else {
+    z.A[0] = pair(lo.a.x, lo.a.z); z.B[0] = pair(lo.a.y, lo.a.w);
+    z.A[1] = pair(lo.b.x, lo.b.z); z.B[1] = pair(lo.b.y, lo.b.w);
+    z.A[2] = pair(hi.a.x, hi.a.z); z.B[2] = pair(hi.a.y, hi.a.w);
+    z.A[3] = pair(hi.b.x, hi.b.z); z.B[3] = pair(hi.b.y, hi.b.w);
+  }
+}
+// The two vectors in memory order.
+template <bool HALF>
+__device__ __forceinline__ void gather(const Sixteen& z, Vec& lo, Vec& hi) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (HALF) {
+      lo.v[i] = z.A[i];
+      hi.v[i] = z.B[i];
+    } else {
+      const float2 a = halves(z.A[i]), b = halves(z.B[i]);
+      Vec& o = i < 2 ? lo : hi;
+      o.v[2 * (i & 1)] = pair(a.x, b.x);
+      o.v[2 * (i & 1) + 1] = pair(a.y, b.y);
+    }
+  }
+}
+template <typename T, bool HALF>
+__device__ __forceinline__ void put(T* at, int half, const Sixteen& z) {
+  Vec lo, hi;
+  gather<HALF>(z, lo, hi);
+  store_vec(at, lo);
+  store_vec(at + half, hi);
+}
+
+// z turned by its angles; `sign` -1 turns back.
+__device__ __forceinline__ void turn(Sixteen& z, const f2 (&c)[4], const f2 (&s)[4], float sign) {
+  const f2 k = pair(sign), nk = pair(-sign);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f2 a = z.A[i];
+    z.A[i] = fma2(mul2(s[i], nk), z.B[i], mul2(a, c[i]));
+    z.B[i] = fma2(mul2(s[i], k), a, mul2(z.B[i], c[i]));
+  }
+}
+__device__ __forceinline__ float dot(const Sixteen& x, const Sixteen& y) {
+  f2 q = mul2(x.A[0], y.A[0]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i) q = fma2(x.A[i], y.A[i], q);
+    q = fma2(x.B[i], y.B[i], q);
+  }
+  const float2 h = halves(q);
+  return h.x + h.y;
+}
+
+// Where a thread works: its worker, its place in a token, its run of tokens.
+struct Place {
+  int slot, lane, lanes, j, head, off;  // off: element offset of the low vector in a token
+  bool on;
+  long long t, end;                     // tokens [t, end), counted b * N + n
+};
 __device__ __forceinline__ Place place(const RopeArgs& p) {
   Place q;
   q.slot = threadIdx.x / p.tpt;
   q.lane = threadIdx.x - q.slot * p.tpt;
   q.lanes = p.d / 16;
-  const int head = q.lane / q.lanes;
-  q.j = q.lane - head * q.lanes;
-  q.on = head < p.H;
-  q.off = head * p.d + q.j * kVec;
+  q.head = q.lane / q.lanes;
+  q.j = q.lane - q.head * q.lanes;
+  q.on = q.head < p.H;
+  q.off = q.head * p.d + q.j * kVec;
   const long long total = (long long)p.B * p.N;
   q.t = ((long long)blockIdx.x * (blockDim.x / p.tpt) + q.slot) * p.chunk;
   q.end = q.t + p.chunk < total ? q.t + p.chunk : total;
   return q;
 }
 
-template <bool HALF>
-__device__ __forceinline__ void read_angles(const float2* cs, int j, int d, float2 (&c)[kVec]) {
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) c[i] = HALF ? cs[j * 8 + i] : i < 4 ? cs[j * 4 + i] : cs[d / 4 + j * 4 + i - 4];
-}
-
-// Block classes: most threads of a block, and the blocks an SM is to hold (the
-// launch bounds set the registers, the grid counts on them).
-template <int MAXT, bool BACK>
-struct Class {
-  static constexpr int kThreads = MAXT == 128 ? (BACK ? 384 : 512) : MAXT == 384 ? (BACK ? 384 : 768) : 1024;  // per SM
-  static constexpr int kBlocks = kThreads / MAXT;
+// Batch entry and token, stepped without divisions.
+struct Token {
+  int b, n;
+  __device__ __forceinline__ Token(const RopeArgs& p, long long t) : b((int)(t / p.N)), n((int)(t - (long long)(t / p.N) * p.N)) {}
+  __device__ __forceinline__ void step(int N) {
+    if (++n == N) { n = 0; ++b; }
+  }
 };
 
-template <typename T, bool HALF, int MAXT>
-__global__ void __launch_bounds__(MAXT, (Class<MAXT, false>::kBlocks)) k_qkv_rope(const __grid_constant__ RopeArgs p) {
-  __shared__ float2 scratch[64];
-  __shared__ float2 table[2][MAXT == 128 ? 32 : 1][kMaxPairs];
-  constexpr bool kAhead = sizeof(T) == 2 && MAXT < 1024;  // the next token is loaded while this one is computed
-  RowSum sum(scratch, p.tpt);
-  const Place pl = place(p);
-  const int half = p.d / 2, head = pl.off / p.d;
-  const float inv_c = 1.f / (float)(p.norm == SVGEAR_QKNORM_TOKEN ? p.H * p.d : p.d);
-  Raw<T> next[3][2];
-  auto fetch = [&](long long t, Raw<T>(&raw)[3][2]) {
-    const int b = (int)(t / p.N), n = (int)(t - (long long)b * p.N);
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      zero_raw(raw[k][0]);
-      zero_raw(raw[k][1]);
-      if (p.in[k] && t < pl.end && pl.on) {
-        const T* x = static_cast<const T*>(p.in[k]) + b * p.batch[k] + n * p.ld[k] + pl.off;
-        load_raw(raw[k][0], x);
-        load_raw(raw[k][1], x + half);
-      }
+// Shared memory: ring stages, then per thread the weights of its elements
+// ([2][4][threads] of 16 bytes), then cos and sin of the tokens in work.
+__device__ __forceinline__ uint8_t* shared_base() {
+  extern __shared__ __align__(128) uint8_t dyn[];
+  return dyn;
+}
+
+// SHARED: in shared memory, each thread its own elements; otherwise (tokens too
+// wide for that) read from global memory, where they stay in the L1.
+template <bool HALF, bool SHARED>
+struct Weights {
+  const RopeArgs& p;
+  const Place& pl;
+  ulonglong2* at;
+  __device__ __forceinline__ void load(int k, Sixteen& z) const {
+    const int o = p.norm == SVGEAR_QKNORM_TOKEN ? pl.off : pl.j * kVec;
+    Raw<float> lo, hi;
+    lo.a = lo.b = hi.a = hi.b = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (p.w[k] && pl.on) {
+      const float4* w = reinterpret_cast<const float4*>(p.w[k] + o);
+      const float4* v = reinterpret_cast<const float4*>(p.w[k] + o + p.d / 2);
+      lo.a = w[0]; lo.b = w[1]; hi.a = v[0]; hi.b = v[1];
     }
-  };
-  if (kAhead) fetch(pl.t, next);
-  for (int it = 0; it < p.chunk; ++it) {
-    const long long t = pl.t + it;
-    const bool live = t < pl.end;
-    if (p.tpt >= 32 && !live) break;  // uniform over the worker
-    const int b = live ? (int)(t / p.N) : 0, n = live ? (int)(t - (long long)b * p.N) : 0;
-    float2* cs = table[it & 1][pl.slot];
-    const long long o = ((long long)(b * p.H + head) * p.out_tokens + n) * p.d + pl.j * kVec;
-    Raw<T> raw[3][2];
-    if (kAhead) {
+    spread<HALF>(lo, hi, z);
+  }
+  __device__ __forceinline__ Weights(const RopeArgs& args, const Place& place)
+      : p(args), pl(place), at(reinterpret_cast<ulonglong2*>(shared_base() + args.ring_bytes) + threadIdx.x) {
+    if (!SHARED || p.norm == SVGEAR_QKNORM_NONE) return;
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        raw[k][0] = next[k][0];
-        raw[k][1] = next[k][1];
+    for (int k = 0; k < 2; ++k) {
+      Sixteen z;
+      load(k, z);
+      const f2 v[8] = {z.A[0], z.A[1], z.A[2], z.A[3], z.B[0], z.B[1], z.B[2], z.B[3]};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) at[(k * 4 + i) * blockDim.x] = make_ulonglong2(v[2 * i], v[2 * i + 1]);
+    }
+  }
+  // z *= weight
+  __device__ __forceinline__ void apply(int k, Sixteen& z) const {
+    Sixteen w;
+    if (SHARED) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const ulonglong2 a = at[(k * 4 + i) * blockDim.x], b = at[(k * 4 + 2 + i) * blockDim.x];
+        w.A[2 * i] = a.x; w.A[2 * i + 1] = a.y;
+        w.B[2 * i] = b.x; w.B[2 * i + 1] = b.y;
       }
     } else {
-      fetch(t, raw);
+      load(k, w);
     }
-    if (p.in[2] && live && pl.on) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      z.A[i] = mul2(z.A[i], w.A[i]);
+      z.B[i] = mul2(z.B[i], w.B[i]);
+    }
+  }
+};
+
+// cos and sin, per token cos[d/2] then sin[d/2].  A block fills the tables of
+// `table_tokens` tokens at once, so that every thread has a pair to compute; a
+// worker inside a warp fills its own token's.  Two buffers: one is filled again
+// only behind the barrier that follows the filling of the other.
+struct Tables {
+  float* base;
+  int half, left, buf, tok;
+  __device__ __forceinline__ Tables(const RopeArgs& p, int slot)
+      : base(reinterpret_cast<float*>(shared_base() + p.ring_bytes + p.weight_bytes)),
+        half(p.d / 2), left(0), buf(1), tok(0) {
+    if (p.tpt <= 32) base += slot * 2 * p.d;
+  }
+  __device__ __forceinline__ void next(const RopeArgs& p, const Token& t, int lane) {
+    if (p.tpt <= 32) {
+      buf ^= 1;
+      float* at = base + buf * p.d;
+      for (int i = lane; i < half; i += p.tpt) {
+        const float2 v = cos_sin(p, t.b, t.n, i);
+        at[i] = v.x;
+        at[half + i] = v.y;
+      }
+      __syncwarp();
+      return;
+    }
+    ++tok;
+    if (left-- == 0) {
+      left = p.table_tokens - 1;
+      tok = 0;
+      buf ^= 1;
+      const int mine = threadIdx.x / half, i = threadIdx.x - mine * half;
+      if (mine < p.table_tokens) {
+        int b = t.b, n = t.n + mine;
+        while (n >= p.N) { n -= p.N; ++b; }
+        if (b < p.B) {
+          const float2 v = cos_sin(p, b, n, i);
+          float* at = base + (buf * p.table_tokens + mine) * p.d;
+          at[i] = v.x;
+          at[half + i] = v.y;
+        }
+      }
+      __syncthreads();
+    }
+  }
+  template <bool HALF>
+  __device__ __forceinline__ void read(const RopeArgs& p, int j, f2 (&c)[4], f2 (&s)[4]) const {
+    const float* at = base + (p.tpt <= 32 ? buf : buf * p.table_tokens + tok) * p.d;
+    const int o0 = HALF ? j * 8 : j * 4, o1 = HALF ? j * 8 + 4 : half / 2 + j * 4;
+    const ulonglong2 c0 = *reinterpret_cast<const ulonglong2*>(at + o0), c1 = *reinterpret_cast<const ulonglong2*>(at + o1);
+    const ulonglong2 s0 = *reinterpret_cast<const ulonglong2*>(at + half + o0), s1 = *reinterpret_cast<const ulonglong2*>(at + half + o1);
+    c[0] = c0.x; c[1] = c0.y; c[2] = c1.x; c[3] = c1.y;
+    s[0] = s0.x; s[1] = s0.y; s[2] = s1.x; s[3] = s1.y;
+  }
+};
+
+// Token-major rows of up to OPS operands: workers inside a warp load them
+// straight into registers, one token ahead; blocks take them from a ring of
+// bulk copies in shared memory.
+template <typename T, int OPS>
+struct Direct {
+  const RopeArgs& p;
+  const Place& pl;
+  Token ahead;
+  long long t;
+  Raw<T> nx[OPS][2];
+  __device__ __forceinline__ void load() {
+#pragma unroll
+    for (int k = 0; k < OPS; ++k) {
+      zero_raw(nx[k][0]);
+      zero_raw(nx[k][1]);
+      if (p.in[k] && t < pl.end && pl.on) {
+        const T* x = static_cast<const T*>(p.in[k]) + ahead.b * p.batch[k] + ahead.n * p.ld[k] + pl.off;
+        load_raw(nx[k][0], x);
+        load_raw(nx[k][1], x + p.d / 2);
+      }
+    }
+  }
+  __device__ __forceinline__ Direct(const RopeArgs& args, const Place& place) : p(args), pl(place), ahead(args, place.t), t(place.t) { load(); }
+  __device__ __forceinline__ void take(Raw<T> (&r)[OPS][2]) {
+#pragma unroll
+    for (int k = 0; k < OPS; ++k) {
+      r[k][0] = nx[k][0];
+      r[k][1] = nx[k][1];
+    }
+    ++t;
+    ahead.step(p.N);
+    load();
+  }
+  __device__ __forceinline__ void release() {}
+};
+
+constexpr int kMaxStages = 8;
+
+template <typename T, int OPS>
+struct Ring {
+  const RopeArgs& p;
+  const Place& pl;
+  Token ahead;       // the next token to be copied
+  long long t;
+  uint32_t row;      // bytes of a token's row
+  uint64_t* full;
+  volatile int* abort_flag;
+  int slot;
+  uint32_t parity;
+  // One thread: the copies of token `ahead` into stage s.
+  __device__ __forceinline__ void issue(int s) {
+    if (t >= pl.end) return;
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int k = 0; k < OPS; ++k) bytes += p.in[k] ? row : 0u;
+    if (bytes) {
+      tc::mbar_arrive_expect_tx(full + s, bytes);
+      const uint32_t dst = tc::smem_u32(shared_base()) + s * OPS * row;
+#pragma unroll
+      for (int k = 0; k < OPS; ++k)
+        if (p.in[k]) tc::bulk_g2s(dst + k * row, static_cast<const T*>(p.in[k]) + ahead.b * p.batch[k] + ahead.n * p.ld[k], row, full + s);
+    }
+    ++t;
+    ahead.step(p.N);
+  }
+  __device__ __forceinline__ Ring(const RopeArgs& args, const Place& place)
+      : p(args), pl(place), ahead(args, place.t), t(place.t), row(args.H * args.d * sizeof(T)), slot(0), parity(0) {
+    __shared__ uint64_t bars[kMaxStages];
+    __shared__ int flag;
+    full = bars;
+    abort_flag = &flag;
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < p.stages; ++i) tc::mbar_init(full + i, 1);
+      flag = 0;
+      tc::mbar_fence_init();
+      for (int i = 0; i < p.stages; ++i) issue(i);
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ void take(Raw<T> (&r)[OPS][2]) {
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < OPS; ++k) any |= p.in[k] != nullptr;
+    // A wait that gives up records it; the block goes on with what is there, so every thread still meets every barrier.
+    if (any) tc::mbar_wait(full + slot, parity, abort_flag, p.status);
+    const uint8_t* at = shared_base() + slot * OPS * row + pl.off * sizeof(T);
+#pragma unroll
+    for (int k = 0; k < OPS; ++k) {
+      zero_raw(r[k][0]);
+      zero_raw(r[k][1]);
+      if (p.in[k] && pl.on) {
+        r[k][0] = *reinterpret_cast<const Raw<T>*>(at + k * row);
+        r[k][1] = *reinterpret_cast<const Raw<T>*>(at + k * row + p.d / 2 * sizeof(T));
+      }
+    }
+  }
+  // Behind a barrier that follows take(): the stage is free for a later token.
+  __device__ __forceinline__ void release() {
+    if (threadIdx.x == 0) issue(slot);
+    if (++slot == p.stages) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+// Block classes: most threads of a block and the threads an SM is to hold (the
+// launch bounds set the registers, the grid and the ring count on them).
+// 0: tokens of up to 512 columns; 1, 2, 3: up to 2,048, 6,144 and 16,384.
+template <int CLS, bool BACK>
+struct Class {
+  static constexpr int kMax = CLS <= 1 ? 128 : CLS == 2 ? 384 : 1024;
+  static constexpr int kThreads = CLS == 0 ? (BACK ? 256 : 512) : CLS == 1 ? (BACK ? 384 : 640) : CLS == 2 ? (BACK ? 384 : 768) : 1024;
+};
+
+// Gradients of Q, K and V of a token, head-major: each thread copies its own
+// vectors into its own slots of shared memory, two tokens ahead (as registers
+// they would spill), so no barrier is needed before it reads them back.
+// Without slots (float32 rows, wide blocks) they are loaded where they are used.
+constexpr int kAheadStages = 3;
+template <typename T>
+constexpr bool ahead_of(int cls) {
+  return sizeof(T) == 2 && cls < 3;
+}
+
+template <typename T, bool AHEAD>
+struct Gradients {
+  static constexpr int kParts = sizeof(Raw<T>) / 16;
+  const RopeArgs& p;
+  const Place& pl;
+  Token ahead;
+  long long t;
+  uint32_t at;
+  int slot;
+  uint8_t* mem;
+  __device__ __forceinline__ const T* source(int k, const Token& tk) const {
+    return static_cast<const T*>(p.grad[k]) + ((long long)(tk.b * p.H + pl.head) * p.out_tokens + tk.n) * p.d + pl.j * kVec;
+  }
+  __device__ __forceinline__ void issue(int s) {
+    if (t < pl.end && pl.on) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (p.grad[k]) {
+          const T* x = source(k, ahead);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < kParts; ++i)
+              tc::cp_async16(at + (((s * 3 + k) * 2 + h) * kParts + i) * blockDim.x * 16, reinterpret_cast<const uint8_t*>(x + h * (p.d / 2)) + i * 16, 16);
+        }
+    }
+    tc::cp_async_commit();
+    ++t;
+    ahead.step(p.N);
+  }
+  __device__ __forceinline__ Gradients(const RopeArgs& args, const Place& place, uint8_t* slots)
+      : p(args), pl(place), ahead(args, place.t), t(place.t), slot(0), mem(slots + threadIdx.x * 16) {
+    at = tc::smem_u32(mem);
+    if (AHEAD)
+      for (int i = 0; i < kAheadStages - 1; ++i) issue(i);
+  }
+  __device__ __forceinline__ void take(const Token& tk, bool mine, Raw<T> (&g)[3][2]) {
+    if (AHEAD) {
+      issue(slot == 0 ? kAheadStages - 1 : slot - 1);  // the slot read last
+      tc::cp_async_wait_group<kAheadStages - 1>();
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        zero_raw(g[k][h]);
+        if (!p.grad[k] || !mine) continue;
+        if (AHEAD) {
+          uint4* r = reinterpret_cast<uint4*>(&g[k][h]);
+#pragma unroll
+          for (int i = 0; i < kParts; ++i)
+            r[i] = *reinterpret_cast<const uint4*>(mem + (((slot * 3 + k) * 2 + h) * kParts + i) * blockDim.x * 16);
+        } else {
+          load_raw(g[k][h], source(k, tk) + h * (p.d / 2));
+        }
+      }
+    if (AHEAD && ++slot == kAheadStages) slot = 0;
+  }
+};
+
+template <typename T, bool HALF, int CLS>
+__global__ void __launch_bounds__(Class<CLS, false>::kMax, (Class<CLS, false>::kThreads / Class<CLS, false>::kMax))
+    k_qkv_rope(const __grid_constant__ RopeArgs p) {
+  __shared__ float2 scratch[64];
+  RowSum sum(scratch, p.tpt);
+  const Place pl = place(p);
+  const int half = p.d / 2;
+  const float inv_c = 1.f / (float)(p.norm == SVGEAR_QKNORM_TOKEN ? p.H * p.d : p.d);
+  const Weights<HALF, CLS != 3> w(p, pl);
+  Tables tables(p, pl.slot);
+  typename std::conditional<CLS == 0, Direct<T, 3>, Ring<T, 3>>::type rows(p, pl);
+  Token tk(p, pl.t);
+  for (int it = 0; it < p.chunk; ++it, tk.step(p.N)) {
+    const bool live = pl.t + it < pl.end;
+    if (p.tpt >= 32 && !live) break;  // uniform over the worker
+    if (!live) tk.b = tk.n = 0;       // lanes of a warp whose other workers still run
+    tables.next(p, tk, pl.lane);
+    Raw<T> raw[3][2];
+    rows.take(raw);
+    const bool mine = live && pl.on;
+    const long long o = ((long long)(tk.b * p.H + pl.head) * p.out_tokens + tk.n) * p.d + pl.j * kVec;
+    if (p.in[2] && mine) {
       T* out = static_cast<T*>(p.out[2]) + o;
       store_raw(out, raw[2][0]);
       store_raw(out + half, raw[2][1]);
     }
-    if (kAhead) fetch(t + 1, next);
-    token_table(p, b, n, cs, pl.lane, p.tpt);
-    if (p.tpt > 32) __syncthreads(); else __syncwarp();
-    float2 c[kVec];
-    read_angles<HALF>(cs, pl.j, p.d, c);
+    Sixteen z[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (!p.in[k]) continue;
-      float lo[kVec], hi[kVec];
-      unpack(raw[k][0], lo);
-      unpack(raw[k][1], hi);
-      if (p.norm != SVGEAR_QKNORM_NONE) {
-        const float inv = rsqrtf(norm_sum(dot16(lo, lo, hi, hi), p.norm, pl.lanes, sum) * inv_c + p.eps);
-        float wl[kVec], wh[kVec];
-        const int wo = p.norm == SVGEAR_QKNORM_TOKEN ? pl.off : pl.j * kVec;
-        if (pl.on && p.w[k]) {
-          load_f8(wl, p.w[k] + wo);
-          load_f8(wh, p.w[k] + wo + half);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) wl[i] = wh[i] = 1.f;
-        }
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          lo[i] *= inv * wl[i];
-          hi[i] *= inv * wh[i];
+    for (int k = 0; k < 2; ++k) spread<HALF>(raw[k][0], raw[k][1], z[k]);
+    if (p.norm != SVGEAR_QKNORM_NONE) {
+      float2 s = make_float2(dot(z[0], z[0]), dot(z[1], z[1]));
+      if (p.norm == SVGEAR_QKNORM_TOKEN) {
+        s = sum(s);
+      } else {
+        for (int i = pl.lanes >> 1; i > 0; i >>= 1) {
+          s.x += __shfl_xor_sync(0xffffffffu, s.x, i);
+          s.y += __shfl_xor_sync(0xffffffffu, s.y, i);
         }
       }
-      turn16<HALF>(lo, hi, c, 1.f);
-      if (live && pl.on) {
-        T* out = static_cast<T*>(p.out[k]) + o;
-        store_vec(out, lo);
-        store_vec(out + half, hi);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const f2 inv = pair(rsqrtf(fmaf(k ? s.y : s.x, inv_c, p.eps)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z[k].A[i] = mul2(z[k].A[i], inv);
+          z[k].B[i] = mul2(z[k].B[i], inv);
+        }
+        w.apply(k, z[k]);
       }
     }
+    f2 c[4], sn[4];
+    tables.read<HALF>(p, pl.j, c, sn);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (p.in[k] && mine) {
+        turn(z[k], c, sn, 1.f);
+        put<T, HALF>(static_cast<T*>(p.out[k]) + o, half, z[k]);
+      }
+    if (CLS != 0 && p.norm != SVGEAR_QKNORM_TOKEN) __syncthreads();  // else the sum's barrier frees the stage
+    rows.release();
   }
 }
 
-template <typename T, bool HALF, int MAXT>
-__global__ void __launch_bounds__(MAXT, (Class<MAXT, true>::kBlocks)) k_qkv_rope_back(const __grid_constant__ RopeArgs p) {
-  __shared__ float2 scratch[64];
-  constexpr int kTable = 2 * (MAXT == 128 ? 32 : 1) * kMaxPairs;
-  constexpr int kRed = MAXT / 32 * kMaxPairs;  // [warps][2 * kMaxPairs] floats, in the table's place at the end
-  __shared__ float2 store[kTable > kRed ? kTable : kRed];
-  constexpr bool kAhead = sizeof(T) == 2 && MAXT < 1024;
+// Backward: g = the gradient turned back; with a norm, n = x inv, u = g w:
+//   dx = inv (u - n mean(u n)) = inv u - x inv^3 sum(u x) / C,  dw += g n,
+// so that sum(x^2) and sum(u x) of Q and of K share one barrier.
+template <typename T, bool HALF, int CLS>
+__global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kThreads / Class<CLS, true>::kMax))
+    k_qkv_rope_back(const __grid_constant__ RopeArgs p) {
+  __shared__ float2 scratch[128];
+  constexpr bool kAhead = ahead_of<T>(CLS);
   RowSum sum(scratch, p.tpt);
   const Place pl = place(p);
-  const int half = p.d / 2, head = pl.off / p.d;
+  const int half = p.d / 2;
   const float inv_c = 1.f / (float)(p.norm == SVGEAR_QKNORM_TOKEN ? p.H * p.d : p.d);
-  float dw[2][2][kVec];
+  const Weights<HALF, CLS != 3> w(p, pl);
+  Tables tables(p, pl.slot);
+  typename std::conditional<CLS == 0, Direct<T, 2>, Ring<T, 2>>::type rows(p, pl);
+  Gradients<T, kAhead> grads(p, pl, shared_base() + p.grads_at);
+  Token tk(p, pl.t);
+  Sixteen dw[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) dw[k][0][i] = dw[k][1][i] = 0.f;
-  Raw<T> next[5][2];  // dQ, dK, dV, q, k
-  auto fetch = [&](long long t, Raw<T>(&raw)[5][2]) {
-    const int b = (int)(t / p.N), n = (int)(t - (long long)b * p.N);
-    const bool ok = t < pl.end && pl.on;
-    const long long o = ((long long)(b * p.H + head) * p.out_tokens + n) * p.d + pl.j * kVec;
-#pragma unroll
-    for (int k = 0; k < 5; ++k) {
-      zero_raw(raw[k][0]);
-      zero_raw(raw[k][1]);
-      const T* x;
-      if (k < 3) {
-        if (!ok || !p.grad[k]) continue;
-        x = static_cast<const T*>(p.grad[k]) + o;
-      } else {
-        if (!ok || p.norm == SVGEAR_QKNORM_NONE || !p.grad[k - 3]) continue;
-        x = static_cast<const T*>(p.in[k - 3]) + b * p.batch[k - 3] + n * p.ld[k - 3] + pl.off;
-      }
-      load_raw(raw[k][0], x);
-      load_raw(raw[k][1], x + half);
-    }
-  };
-  if (kAhead) fetch(pl.t, next);
-  for (int it = 0; it < p.chunk; ++it) {
-    const long long t = pl.t + it;
-    const bool live = t < pl.end;
+    for (int i = 0; i < 4; ++i) dw[k].A[i] = dw[k].B[i] = pair(0.f);
+  for (int it = 0; it < p.chunk; ++it, tk.step(p.N)) {
+    const bool live = pl.t + it < pl.end;
     if (p.tpt >= 32 && !live) break;
-    const int b = live ? (int)(t / p.N) : 0, n = live ? (int)(t - (long long)b * p.N) : 0;
-    const long long go = b * p.out_batch + n * p.out_ld + pl.off;
-    float2* cs = store + ((it & 1) * (MAXT == 128 ? 32 : 1) + pl.slot) * kMaxPairs;
-    Raw<T> raw[5][2];
-    if (kAhead) {
-#pragma unroll
-      for (int k = 0; k < 5; ++k) {
-        raw[k][0] = next[k][0];
-        raw[k][1] = next[k][1];
-      }
-    } else {
-      fetch(t, raw);
-    }
-    if (p.grad[2] && live && pl.on) {
+    if (!live) tk.b = tk.n = 0;
+    const bool mine = live && pl.on;
+    const long long go = tk.b * p.out_batch + tk.n * p.out_ld + pl.off;
+    Raw<T> g[3][2];
+    grads.take(tk, mine, g);
+    if (p.grad[2] && mine) {
       T* out = static_cast<T*>(p.out[2]) + go;
-      store_raw(out, raw[2][0]);
-      store_raw(out + half, raw[2][1]);
+      store_raw(out, g[2][0]);
+      store_raw(out + half, g[2][1]);
     }
-    if (kAhead) fetch(t + 1, next);
-    token_table(p, b, n, cs, pl.lane, p.tpt);
-    if (p.tpt > 32) __syncthreads(); else __syncwarp();
-    float2 c[kVec];
-    read_angles<HALF>(cs, pl.j, p.d, c);
+    tables.next(p, tk, pl.lane);
+    Raw<T> raw[2][2];
+    rows.take(raw);
+    Sixteen z[2];
+    {
+      f2 c[4], sn[4];
+      tables.read<HALF>(p, pl.j, c, sn);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (!p.grad[k]) continue;
-      float lo[kVec], hi[kVec];
-      unpack(raw[k][0], lo);
-      unpack(raw[k][1], hi);
-      turn16<HALF>(lo, hi, c, -1.f);
-      if (p.norm != SVGEAR_QKNORM_NONE) {
-        float nl[kVec], nh[kVec];
-        unpack(raw[3 + k][0], nl);
-        unpack(raw[3 + k][1], nh);
-        const float inv = rsqrtf(norm_sum(dot16(nl, nl, nh, nh), p.norm, pl.lanes, sum) * inv_c + p.eps);
+      for (int k = 0; k < 2; ++k) {
+        spread<HALF>(g[k][0], g[k][1], z[k]);
+        turn(z[k], c, sn, -1.f);
+      }
+    }
+    if (p.norm != SVGEAR_QKNORM_NONE) {
+      Sixteen x[2];
+      float2 s[2];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          nl[i] *= inv;
-          nh[i] *= inv;
-          dw[k][0][i] = fmaf(lo[i], nl[i], dw[k][0][i]);
-          dw[k][1][i] = fmaf(hi[i], nh[i], dw[k][1][i]);
-        }
-        if (pl.on && p.w[k]) {
-          const int wo = p.norm == SVGEAR_QKNORM_TOKEN ? pl.off : pl.j * kVec;
-          float wl[kVec], wh[kVec];
-          load_f8(wl, p.w[k] + wo);
-          load_f8(wh, p.w[k] + wo + half);
+      for (int k = 0; k < 2; ++k) {
+        spread<HALF>(raw[k][0], raw[k][1], x[k]);
+        Sixteen u = z[k];
+        w.apply(k, u);
+        s[k] = make_float2(dot(x[k], x[k]), dot(u, x[k]));
+      }
+      if (p.norm == SVGEAR_QKNORM_TOKEN) {
+        sum.both(s[0], s[1]);
+      } else {
+        for (int i = pl.lanes >> 1; i > 0; i >>= 1)
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) {
-            lo[i] *= wl[i];
-            hi[i] *= wh[i];
+          for (int k = 0; k < 2; ++k) {
+            s[k].x += __shfl_xor_sync(0xffffffffu, s[k].x, i);
+            s[k].y += __shfl_xor_sync(0xffffffffu, s[k].y, i);
           }
-        }
-        const float mean = norm_sum(dot16(lo, nl, hi, nh), p.norm, pl.lanes, sum) * inv_c;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          lo[i] = inv * (lo[i] - nl[i] * mean);
-          hi[i] = inv * (hi[i] - nh[i] * mean);
-        }
       }
-      if (live && pl.on) {
-        T* out = static_cast<T*>(p.out[k]) + go;
-        store_vec(out, lo);
-        store_vec(out + half, hi);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float r = rsqrtf(fmaf(s[k].x, inv_c, p.eps));
+        const f2 inv = pair(r), m = pair(-(s[k].y * inv_c) * r * r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[k].A[i] = mul2(x[k].A[i], inv);
+          x[k].B[i] = mul2(x[k].B[i], inv);
+          dw[k].A[i] = fma2(z[k].A[i], x[k].A[i], dw[k].A[i]);
+          dw[k].B[i] = fma2(z[k].B[i], x[k].B[i], dw[k].B[i]);
+        }
+        w.apply(k, z[k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z[k].A[i] = fma2(x[k].A[i], m, mul2(z[k].A[i], inv));
+          z[k].B[i] = fma2(x[k].B[i], m, mul2(z[k].B[i], inv));
+        }
       }
     }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (p.grad[k] && mine) put<T, HALF>(static_cast<T*>(p.out[k]) + go, half, z[k]);
+    if (CLS != 0 && p.norm != SVGEAR_QKNORM_TOKEN) __syncthreads();
+    rows.release();
   }
   if (!p.part) return;
   const long long worker = (long long)blockIdx.x * (blockDim.x / p.tpt) + pl.slot;
-  const bool mine = pl.t < (long long)p.B * p.N;  // workers without a token have no slot
+  const bool has = pl.t < (long long)p.B * p.N;  // workers without a token have no slot
   if (p.norm == SVGEAR_QKNORM_TOKEN) {
-    if (mine && pl.on)
+    if (has && pl.on)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float* part = p.part + ((size_t)worker * 2 + k) * p.H * p.d + pl.off;
-        store_vec(part, dw[k][0]);
-        store_vec(part + half, dw[k][1]);
-      }
+      for (int k = 0; k < 2; ++k) put<float, HALF>(p.part + ((size_t)worker * 2 + k) * p.H * p.d + pl.off, half, dw[k]);
     return;
   }
   // Per-head weights: add the heads of this worker, in a warp, then over its warps.
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        for (int s = pl.lanes; s < (p.tpt < 32 ? p.tpt : 32); s <<= 1)
-          dw[k][h][i] += __shfl_xor_sync(0xffffffffu, dw[k][h][i], s);
-  if (p.tpt <= 32) {
-    if (mine && pl.lane < pl.lanes)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float* part = p.part + ((size_t)worker * 2 + k) * p.d + pl.j * kVec;
-        store_vec(part, dw[k][0]);
-        store_vec(part + half, dw[k][1]);
+    for (int i = 0; i < 4; ++i) {
+      float2 a = halves(dw[k].A[i]), b = halves(dw[k].B[i]);
+      for (int s = pl.lanes; s < (p.tpt < 32 ? p.tpt : 32); s <<= 1) {
+        a.x += __shfl_xor_sync(0xffffffffu, a.x, s);
+        a.y += __shfl_xor_sync(0xffffffffu, a.y, s);
+        b.x += __shfl_xor_sync(0xffffffffu, b.x, s);
+        b.y += __shfl_xor_sync(0xffffffffu, b.y, s);
       }
+      dw[k].A[i] = pair(a.x, a.y);
+      dw[k].B[i] = pair(b.x, b.y);
+    }
+  if (p.tpt <= 32) {
+    if (has && pl.lane < pl.lanes)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) put<float, HALF>(p.part + ((size_t)worker * 2 + k) * p.d + pl.j * kVec, half, dw[k]);
     return;
   }
-  float(*wred)[2 * kMaxPairs] = reinterpret_cast<float(*)[2 * kMaxPairs]>(store);
+  float* red = reinterpret_cast<float*>(shared_base());  // [warps][d], over the ring, whose copies have all been taken
   for (int k = 0; k < 2; ++k) {
     __syncthreads();
-    if ((threadIdx.x & 31) < pl.lanes)
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        wred[threadIdx.x >> 5][pl.j * kVec + i] = dw[k][0][i];
-        wred[threadIdx.x >> 5][half + pl.j * kVec + i] = dw[k][1][i];
-      }
+    if ((threadIdx.x & 31) < pl.lanes) put<float, HALF>(red + (threadIdx.x >> 5) * p.d + pl.j * kVec, half, dw[k]);
     __syncthreads();
     for (int i = threadIdx.x; i < p.d; i += blockDim.x) {
       float s = 0.f;
-      for (int w = 0; w < p.tpt / 32; ++w) s += wred[w][i];
-      if (mine) p.part[((size_t)worker * 2 + k) * p.d + i] = s;
+      for (int v = 0; v < p.tpt / 32; ++v) s += red[v * p.d + i];
+      if (has) p.part[((size_t)worker * 2 + k) * p.d + i] = s;
     }
   }
 }
@@ -410,31 +705,50 @@ __global__ void __launch_bounds__(32 * kSumLanes) k_rope_weight_sums(const float
 }
 
 struct Shape {
-  int tpt, block, cls, chunk, grid;
+  int cls, tpt, block, chunk, grid, stages, ring_bytes, weight_bytes, table_tokens, grads_at, smem;
   long long workers;
 };
+
+constexpr int kSmemPerSm = 228 * 1024, kSmemPerBlock = 3072;  // 1 KB per block is the system's, the rest static arrays
 
 Shape rope_shape(const svgear_rope_params* p, bool back) {
   Shape s;
   const int items = p->H * p->d / 16;
+  const bool normed = p->norm != SVGEAR_QKNORM_NONE;
+  int threads;
   if (items <= 32) {
+    s.cls = 0;
     s.tpt = items <= 4 ? 4 : items <= 8 ? 8 : items <= 16 ? 16 : 32;
     s.block = 128;
+    threads = back ? Class<0, true>::kThreads : Class<0, false>::kThreads;
   } else {
     s.tpt = s.block = (items + 31) / 32 * 32;
+    s.cls = s.block <= 128 ? 1 : s.block <= 384 ? 2 : 3;
+    threads = s.cls == 1   ? (back ? Class<1, true>::kThreads : Class<1, false>::kThreads)
+              : s.cls == 2 ? (back ? Class<2, true>::kThreads : Class<2, false>::kThreads)
+                           : Class<3, true>::kThreads;
   }
-  s.cls = s.block <= 128 ? 128 : s.block <= 384 ? 384 : 1024;
   const int per = s.block / s.tpt;
   const long long tokens = (long long)p->B * p->N;
-  // As many blocks as the SMs hold at once, each with a run of tokens.
-  const int threads = s.cls == 1024 ? 1024
-                      : s.cls == 384 ? (back ? Class<384, true>::kThreads : Class<384, false>::kThreads)
-                                     : (back ? Class<128, true>::kThreads : Class<128, false>::kThreads);
-  long long want = std::min(tokens, 148LL * (threads / s.block) * per);
+  s.table_tokens = s.cls == 0 ? per : std::max(1, s.block / (p->d / 2));
+  s.weight_bytes = normed && s.cls != 3 ? 128 * s.block : 0;
+  const int front = s.weight_bytes + 2 * s.table_tokens * p->d * (int)sizeof(float);
+  const int fixed = front + (back && p->dtype == DT_BF16 && ahead_of<bf16>(s.cls) ? kAheadStages * 6 * 16 * s.block : 0);
+  // The forward pass brings q, k and v through the ring, the backward pass q and k where a norm needs them.
+  const int stage = s.cls == 0 ? 0 : (back ? (normed ? 2 : 0) : 3) * p->H * p->d * (p->dtype == DT_F32 ? 4 : 2);
+  int blocks = std::max(1, std::min(threads / s.block, 8));
+  auto stages = [&]() { return stage ? (kSmemPerSm / blocks - kSmemPerBlock - fixed) / stage : 1; };
+  while (stage && blocks > 1 && stages() < 2) --blocks;
+  // As many workers as the SMs hold at once, each with a run of tokens.
+  long long want = std::min(tokens, 148LL * blocks * per);
   if (back) want = std::min(want, 4096LL);
   s.chunk = (int)((tokens + want - 1) / want);
   s.workers = (tokens + s.chunk - 1) / s.chunk;
   s.grid = (int)((s.workers + per - 1) / per);
+  s.stages = std::max(1, std::min({stages(), kMaxStages, s.chunk}));
+  s.ring_bytes = s.stages * stage;
+  s.grads_at = s.ring_bytes + front;
+  s.smem = s.ring_bytes + fixed;
   return s;
 }
 
@@ -456,6 +770,12 @@ RopeArgs rope_args(const svgear_rope_params* p, const float* wq, const float* wk
   a.norm = p->norm;
   a.tpt = s.tpt;
   a.chunk = s.chunk;
+  a.stages = s.stages;
+  a.ring_bytes = s.ring_bytes;
+  a.table_tokens = s.table_tokens;
+  a.weight_bytes = s.weight_bytes;
+  a.grads_at = s.grads_at;
+  a.status = status_word();
   a.pairs0 = p->axes[0] / 2;
   a.pairs01 = a.pairs0 + p->axes[1] / 2;
   a.pairs = a.pairs01 + p->axes[2] / 2;
@@ -473,24 +793,31 @@ RopeArgs rope_args(const svgear_rope_params* p, const float* wq, const float* wk
   return a;
 }
 
-template <typename T, bool HALF, int MAXT>
-void launch_class(const RopeArgs& a, const Shape& s, bool back, cudaStream_t st) {
-  if (back) k_qkv_rope_back<T, HALF, MAXT><<<s.grid, s.block, 0, st>>>(a);
-  else k_qkv_rope<T, HALF, MAXT><<<s.grid, s.block, 0, st>>>(a);
+template <typename T, bool HALF, int CLS>
+cudaError_t launch_class(const RopeArgs& a, const Shape& s, bool back, cudaStream_t st) {
+  const auto kernel = back ? k_qkv_rope_back<T, HALF, CLS> : k_qkv_rope<T, HALF, CLS>;
+  if (s.smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<s.grid, s.block, s.smem, st>>>(a);
   note_launch();
+  return cudaGetLastError();
 }
 
 template <typename T, bool HALF>
-void launch_half(const RopeArgs& a, const Shape& s, bool back, cudaStream_t st) {
-  if (s.cls == 128) launch_class<T, HALF, 128>(a, s, back, st);
-  else if (s.cls == 384) launch_class<T, HALF, 384>(a, s, back, st);
-  else launch_class<T, HALF, 1024>(a, s, back, st);
+cudaError_t launch_half(const RopeArgs& a, const Shape& s, bool back, cudaStream_t st) {
+  if (s.cls == 0) return launch_class<T, HALF, 0>(a, s, back, st);
+  if (s.cls == 1) return launch_class<T, HALF, 1>(a, s, back, st);
+  if (s.cls == 2) return launch_class<T, HALF, 2>(a, s, back, st);
+  return launch_class<T, HALF, 3>(a, s, back, st);
 }
 
-template <typename T>
-void launch_rope(const RopeArgs& a, const Shape& s, bool half, bool back, cudaStream_t st) {
-  if (half) launch_half<T, true>(a, s, back, st);
-  else launch_half<T, false>(a, s, back, st);
+cudaError_t launch_rope(const RopeArgs& a, const Shape& s, const svgear_rope_params* p, bool back, cudaStream_t st) {
+  if (!a.status) return cudaErrorInvalidValue;
+  const bool half = p->pairing == SVGEAR_PAIR_HALF;
+  if (p->dtype == DT_F32) return half ? launch_half<float, true>(a, s, back, st) : launch_half<float, false>(a, s, back, st);
+  return half ? launch_half<bf16, true>(a, s, back, st) : launch_half<bf16, false>(a, s, back, st);
 }
 
 }  // namespace
@@ -503,10 +830,7 @@ cudaError_t qkv_rope_run(const void* const in[3], const float* wq, const float* 
     a.in[k] = in[k];
     a.out[k] = out[k];
   }
-  const bool half = p->pairing == SVGEAR_PAIR_HALF;
-  if (p->dtype == DT_F32) launch_rope<float>(a, s, half, false, st);
-  else launch_rope<bf16>(a, s, half, false, st);
-  return cudaGetLastError();
+  return launch_rope(a, s, p, false, st);
 }
 
 size_t qkv_rope_back_ws_bytes(const svgear_rope_params* p) {
@@ -523,14 +847,11 @@ cudaError_t qkv_rope_back_run(const void* const grad[3], const void* const in[2]
   for (int k = 0; k < 3; ++k) {
     a.grad[k] = grad[k];
     a.out[k] = out[k];
-    if (k < 2) a.in[k] = in[k];
+    if (k < 2 && grad[k]) a.in[k] = in[k];  // null without a norm
   }
   const bool sums = p->norm != SVGEAR_QKNORM_NONE && (dwq || dwk);
   a.part = sums ? static_cast<float*>(ws) : nullptr;
-  const bool half = p->pairing == SVGEAR_PAIR_HALF;
-  if (p->dtype == DT_F32) launch_rope<float>(a, s, half, true, st);
-  else launch_rope<bf16>(a, s, half, true, st);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_rope(a, s, p, true, st);
   if (e == cudaSuccess && sums) {
     const int C = p->norm == SVGEAR_QKNORM_TOKEN ? p->H * p->d : p->d;
     k_rope_weight_sums<<<dim3((C + 31) / 32, 2), 32 * kSumLanes, 0, st>>>(a.part, s.workers, C, dwq, dwk);

@@ -181,6 +181,20 @@ struct RowSum {
     }
     return v;
   }
+  // Two pairs behind one barrier; `scratch` has two more halves for it ([4][32]).
+  __device__ __forceinline__ void both(float2& a, float2& b) {
+    a = lanes(a);
+    b = lanes(b);
+    if (width > 32) {
+      float2* s = scratch + 64 + phase * 32;
+      if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = b;
+      a = trade(a);
+      const int i = threadIdx.x & mask;
+      b = i < width >> 5 ? s[i] : make_float2(0.f, 0.f);
+      a = make_float2(warps(a.x), warps(a.y));
+      b = make_float2(warps(b.x), warps(b.y));
+    }
+  }
   __device__ __forceinline__ float operator()(float v) {
     v = lanes(v);
     return width > 32 ? warps(trade(make_float2(v, 0.f)).x) : v;

@@ -20,6 +20,7 @@ inline int esize(int dtype) { return dtype == SVGEAR_BF16 ? 2 : 4; }
 
 constexpr int kMaxNormCols = 8192;
 constexpr int kMaxTokenCols = 16384;
+constexpr int kMaxRows = 1 << 30;  // row counters are int, and run ahead by a few stages
 
 int check_norm(const svgear_norm_params* p) {
   if (!p || p->N < 1 || p->D < 1 || p->G < 1) return SVGEAR_ERR_INVALID;
@@ -28,7 +29,7 @@ int check_norm(const svgear_norm_params* p) {
   if (!(p->eps > 0.f) || std::isinf(p->eps) || !std::isfinite(p->res_scale)) return SVGEAR_ERR_INVALID;
   if (!known_dtype(p->dtype) || !known_dtype(p->res_dtype)) return SVGEAR_ERR_UNSUPPORTED;
   if (p->res_dtype == SVGEAR_BF16 && p->dtype == SVGEAR_F32) return SVGEAR_ERR_UNSUPPORTED;
-  if (p->D % 8 || p->D > kMaxNormCols) return SVGEAR_ERR_UNSUPPORTED;
+  if (p->D % 8 || p->D > kMaxNormCols || p->N > kMaxRows) return SVGEAR_ERR_UNSUPPORTED;
   return SVGEAR_OK;
 }
 
@@ -58,7 +59,7 @@ int check_rope(const svgear_rope_params* p) {
   if (p->d != 64 && p->d != 128) return SVGEAR_ERR_UNSUPPORTED;
   if (turned > p->d) return SVGEAR_ERR_INVALID;
   if ((long long)p->H * p->d > kMaxTokenCols) return SVGEAR_ERR_UNSUPPORTED;
-  if ((long long)p->B * p->N >= (1LL << 31) || (long long)p->B * p->H >= (1LL << 31)) return SVGEAR_ERR_UNSUPPORTED;
+  if ((long long)p->B * p->N > kMaxRows || (long long)p->B * p->H >= (1LL << 31)) return SVGEAR_ERR_UNSUPPORTED;
   return SVGEAR_OK;
 }
 

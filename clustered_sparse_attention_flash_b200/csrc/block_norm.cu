@@ -61,7 +61,8 @@ struct Columns {
   int col[V];
   bool on[V];
   float inv_d, d, inv_own, n, inv_n;
-  __device__ __forceinline__ void init(int D, int tpr, int lane, const RowSum& sum) {
+  template <typename SUM>
+  __device__ __forceinline__ void init(int D, int tpr, int lane, const SUM&) {
     d = (float)D;
     inv_d = 1.f / d;
 #pragma unroll
@@ -77,7 +78,7 @@ struct Columns {
     };
     const float own = tpr > 32 ? columns_of(lane >> 5) : d;
     inv_own = own > 0.f ? 1.f / own : 0.f;
-    const int other = threadIdx.x & sum.mask;
+    const int other = threadIdx.x & SUM::kMask;
     n = tpr > 32 && other < tpr >> 5 ? columns_of(other) : 0.f;
     inv_n = n > 0.f ? 1.f / n : 0.f;
   }
@@ -124,11 +125,11 @@ __device__ __forceinline__ float over(float s, float d, float inv_d) {
 // are joined by
 //   squares = sum_w squares_w + n_w (mean_w - mean)^2,
 // every term of which is a square: nothing cancels, whatever the mean.
-template <int V>
-__device__ __forceinline__ float2 statistics(const Vec (&f)[V], const Columns<V>& c, int kind, float eps, RowSum& sum) {
+template <int V, typename SUM>
+__device__ __forceinline__ float2 statistics(const Vec (&f)[V], const Columns<V>& c, int kind, float eps, SUM& sum) {
   if (kind == SVGEAR_NORM_RMS) return make_float2(0.f, rsqrtf(fmaf(sum(squares(f, c, 0.f)), c.inv_d, eps)));
   const float s = sum.lanes(total(f, c));
-  if (sum.width <= 32) {
+  if (!SUM::kBlock) {
     const float mean = over(s, c.d, c.inv_d);
     return make_float2(mean, rsqrtf(fmaf(sum.lanes(squares(f, c, mean)), c.inv_d, eps)));
   }
@@ -138,64 +139,85 @@ __device__ __forceinline__ float2 statistics(const Vec (&f)[V], const Columns<V>
   return make_float2(mean, rsqrtf(fmaf(sum.warps(fmaf(c.n * e, e, v.y)), c.inv_d, eps)));
 }
 
-// f becomes the normalised row; returns 1 / deviation.
+// f = (f - mean) inv
 template <int V>
-__device__ __forceinline__ float normalise(Vec (&f)[V], const Columns<V>& c, int kind, float eps, RowSum& sum) {
-  if (kind == SVGEAR_NORM_NONE) return 1.f;
-  const float2 st = statistics(f, c, kind, eps, sum);
+__device__ __forceinline__ void apply(Vec (&f)[V], float2 st) {
   const f2 m = pair(-st.x), inv = pair(st.y);
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[v].v[i] = mul2(add2(f[v].v[i], m), inv);
+}
+
+// f becomes the normalised row; returns 1 / deviation.
+template <int V, typename SUM>
+__device__ __forceinline__ float normalise(Vec (&f)[V], const Columns<V>& c, int kind, float eps, SUM& sum) {
+  if (kind == SVGEAR_NORM_NONE) return 1.f;
+  const float2 st = statistics(f, c, kind, eps, sum);
+  apply<V>(f, st);
   return st.y;
 }
 
 // Rows of a worker, one at a time, behind one interface: narrow rows straight
 // from global memory (the next row is loaded while this one is computed), wide
 // rows through a ring of bulk copies in shared memory, so that the bytes in
-// flight do not depend on how many threads are resident.  `take` fills the
-// vectors of this thread with its columns of `row`; rows come in order.  An
-// operand that is not given, or a column that does not exist, reads as zeros.
-template <typename TX, typename TY, int V>
-struct Row {
-  Raw<TX> x[V], dr[V];
-  Raw<TY> y[V], dh[V];
-};
+// flight do not depend on how many threads are resident.  Rows come in order;
+// operand k of the current row is read when it is needed.  Threads without a
+// column read the last ones: they add to no sum and store nothing.
+enum Operand { kX = 0, kY = 1, kDr = 2, kDh = 3 };
 
 template <typename TX, typename TY, int OPS, int V>
 struct Direct {
   const NormArgs& p;
   const Columns<V>& c;
-  long long end;
-  Row<TX, TY, V> next;
+  int end;
+  Raw<TX> x[V], dr[V], nx[V], ndr[V];
+  Raw<TY> y[V], dh[V], ny[V], ndh[V];
   template <typename T>
   __device__ __forceinline__ void one(Raw<T>& r, const void* base, long long at, bool ok) {
     zero_raw(r);
     if (ok && base) load_raw(r, static_cast<const T*>(base) + at);
   }
-  __device__ __forceinline__ void load(long long row) {
+  __device__ __forceinline__ void load(int row) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const long long at = row * p.D + c.col[v];
+      const long long at = (long long)row * p.D + c.col[v];
       const bool ok = c.on[v] && row < end;
-      one(next.x[v], p.x, at, ok);
-      one(next.y[v], p.y, at, ok);
+      one(nx[v], p.x, at, ok);
+      one(ny[v], p.y, at, ok);
       if (OPS == 4) {
-        one(next.dr[v], p.dr, at, ok);
-        one(next.dh[v], p.dh, at, ok);
+        one(ndr[v], p.dr, at, ok);
+        one(ndh[v], p.dh, at, ok);
       }
     }
   }
-  __device__ __forceinline__ Direct(const NormArgs& args, const Columns<V>& cols, long long first, long long last)
+  __device__ __forceinline__ Direct(const NormArgs& args, const Columns<V>& cols, int first, int last)
       : p(args), c(cols), end(last) {
     load(first);
   }
-  __device__ __forceinline__ void take(long long row, Row<TX, TY, V>& r) {
-    r = next;
+  __device__ __forceinline__ void take(int row) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      x[v] = nx[v];
+      y[v] = ny[v];
+      if (OPS == 4) {
+        dr[v] = ndr[v];
+        dh[v] = ndh[v];
+      }
+    }
     load(row + 1);
   }
-  __device__ __forceinline__ void release(long long) {}
+  template <int K>
+  __device__ __forceinline__ void read(Vec (&f)[V]) const {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (K == kX) unpack(x[v], f[v]);
+      if (K == kY) unpack(y[v], f[v]);
+      if (K == kDr) unpack(dr[v], f[v]);
+      if (K == kDh) unpack(dh[v], f[v]);
+    }
+  }
+  __device__ __forceinline__ void release(int) {}
 };
 
 constexpr int kMaxStages = 16;
@@ -203,37 +225,40 @@ constexpr int kMaxStages = 16;
 template <typename TX, typename TY, int OPS, int V>
 struct Ring {
   const NormArgs& p;
-  const Columns<V>& c;
-  long long end;
+  int end;
   uint32_t bx, by, stage;  // bytes of a row of either type, of a stage
+  uint32_t col[V];
   uint8_t* buf;
   uint64_t* full;
   volatile int* abort_flag;
-  int slot;         // the stage of the row that is next taken,
+  int slot;         // the stage of the current row,
   uint32_t parity;  // and the parity of its phase
   // One thread: the copies of `row` into stage s.
-  __device__ __forceinline__ void issue(long long row, int s) {
+  __device__ __forceinline__ void issue(int row, int s) {
     if (row >= end) return;
     tc::mbar_arrive_expect_tx(full + s, bx + (p.y ? by : 0u) + (OPS == 4 ? (p.dr ? bx : 0u) + (p.dh ? by : 0u) : 0u));
     const uint32_t dst = tc::smem_u32(buf) + s * stage;
-    tc::bulk_g2s(dst, static_cast<const char*>(p.x) + row * bx, bx, full + s);
-    if (p.y) tc::bulk_g2s(dst + bx, static_cast<const char*>(p.y) + row * by, by, full + s);
+    tc::bulk_g2s(dst, static_cast<const char*>(p.x) + (long long)row * bx, bx, full + s);
+    if (p.y) tc::bulk_g2s(dst + bx, static_cast<const char*>(p.y) + (long long)row * by, by, full + s);
     if (OPS == 4) {
-      if (p.dr) tc::bulk_g2s(dst + bx + by, static_cast<const char*>(p.dr) + row * bx, bx, full + s);
-      if (p.dh) tc::bulk_g2s(dst + 2 * bx + by, static_cast<const char*>(p.dh) + row * by, by, full + s);
+      if (p.dr) tc::bulk_g2s(dst + bx + by, static_cast<const char*>(p.dr) + (long long)row * bx, bx, full + s);
+      if (p.dh) tc::bulk_g2s(dst + 2 * bx + by, static_cast<const char*>(p.dh) + (long long)row * by, by, full + s);
     }
   }
-  __device__ __forceinline__ Ring(const NormArgs& args, const Columns<V>& cols, long long first, long long last)
-      : p(args), c(cols), end(last), slot(0), parity(0) {
+  __device__ __forceinline__ Ring(const NormArgs& args, const Columns<V>& cols, int first, int last)
+      : p(args), end(last), slot(-1), parity(1) {
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ uint64_t bars[kMaxStages];
     __shared__ int flag;
     bx = p.D * sizeof(TX);
     by = p.D * sizeof(TY);
     stage = (OPS / 2) * (bx + by);
+#pragma unroll
+    for (int v = 0; v < V; ++v) col[v] = min(cols.col[v], p.D - kVec);
     buf = dyn;
     full = bars;
     abort_flag = &flag;
+    slot = p.stages - 1;
     if (threadIdx.x == 0) {
       for (int i = 0; i < p.stages; ++i) tc::mbar_init(full + i, 1);
       flag = 0;
@@ -242,54 +267,48 @@ struct Ring {
     }
     __syncthreads();
   }
-  template <typename T>
-  __device__ __forceinline__ void one(Raw<T>& r, const void* base, const uint8_t* at, int v) {
-    zero_raw(r);
-    if (c.on[v] && base) r = *reinterpret_cast<const Raw<T>*>(at + c.col[v] * sizeof(T));
-  }
-  __device__ __forceinline__ void take(long long row, Row<TX, TY, V>& r) {
-    // A wait that gives up records it; the block goes on with what is there, so every thread still meets every barrier.
-    tc::mbar_wait(full + slot, parity, abort_flag, p.status);
-    const uint8_t* at = buf + slot * stage;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      one(r.x[v], p.x, at, v);
-      one(r.y[v], p.y, at + bx, v);
-      if (OPS == 4) {
-        one(r.dr[v], p.dr, at + bx + by, v);
-        one(r.dh[v], p.dh, at + 2 * bx + by, v);
-      }
-    }
-  }
-  // Behind a barrier that follows take(row): the stage is free for a later row.
-  __device__ __forceinline__ void release(long long row) {
-    if (threadIdx.x == 0) issue(row + p.stages, slot);
+  __device__ __forceinline__ void take(int) {
     if (++slot == p.stages) {
       slot = 0;
       parity ^= 1;
     }
+    // A wait that gives up records it; the block goes on with what is there, so every thread still meets every barrier.
+    tc::mbar_wait(full + slot, parity, abort_flag, p.status);
+  }
+  template <int K>
+  __device__ __forceinline__ void read(Vec (&f)[V]) const {
+    const uint8_t* at = buf + slot * stage + (K == kX ? 0u : K == kY ? bx : K == kDr ? bx + by : 2 * bx + by);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (K == kX || K == kDr) unpack(*reinterpret_cast<const Raw<TX>*>(at + col[v] * sizeof(TX)), f[v]);
+      else unpack(*reinterpret_cast<const Raw<TY>*>(at + col[v] * sizeof(TY)), f[v]);
+    }
+  }
+  // Behind a barrier that every thread reached after its last read of `row`.
+  __device__ __forceinline__ void release(int row) {
+    if (threadIdx.x == 0) issue(row + p.stages, slot);
   }
 };
 
 // The worker of a thread and its rows, up to the last group's end.
 struct Place {
-  long long worker, row, end;
-  int lane;
+  int worker, row, end, lane;
 };
 __device__ __forceinline__ Place place(const NormArgs& p) {
   Place q;
   const int slot = threadIdx.x / p.tpr;
-  q.worker = (long long)blockIdx.x * (blockDim.x / p.tpr) + slot;
+  q.worker = blockIdx.x * (blockDim.x / p.tpr) + slot;
   q.lane = threadIdx.x - slot * p.tpr;
-  q.row = q.worker * p.chunk;
-  q.end = min(q.row + p.chunk, (long long)group_end(p, p.G - 1));
+  const long long first = (long long)q.worker * p.chunk;
+  q.end = (int)min(first + p.chunk, (long long)group_end(p, p.G - 1));
+  q.row = (int)min(first, (long long)p.N);
   return q;
 }
 
 // The coefficients of this thread's columns in group g: (1 + scale) weight,
-// bias (1 + scale) + shift, gate post_weight.  Narrow rows keep them in
-// registers; wide rows keep all but the first in shared memory, each thread its
-// own columns: as registers they would cost the second block per SM (or spill
+// bias (1 + scale) + shift (forward), gate post_weight.  Narrow rows keep them in
+// registers; wide rows keep two in shared memory, each thread its own columns,
+// and the forward pass the first in registers: as registers they would cost the second block per SM (or spill
 // to local memory, which has no L1 left beside the ring: 879 us against 632 at
 // 75,600 x 5,120).
 template <int V, bool SHARED>
@@ -299,6 +318,7 @@ struct Coefficients<V, false> {
   Vec a[V], b[V], g[V];
   __device__ __forceinline__ Coefficients(const NormArgs&, const Columns<V>&, uint8_t*) {}
   __device__ __forceinline__ void put(int which, int v, const Vec& t) { (which == 0 ? b : g)[v] = t; }
+  __device__ __forceinline__ Vec get_a(int v) const { return a[v]; }
   __device__ __forceinline__ Vec get_b(int v) const { return b[v]; }
   __device__ __forceinline__ Vec get_g(int v) const { return g[v]; }
 };
@@ -312,6 +332,7 @@ struct Coefficients<V, true> {
     for (int v = 0; v < V; ++v) at[v] = reinterpret_cast<float*>(mem) + (c.on[v] ? c.col[v] : 0);
   }
   __device__ __forceinline__ void put(int which, int v, const Vec& t) { store_vec(at[v] + which * D, t); }
+  __device__ __forceinline__ Vec get_a(int v) const { return get_b(v); }  // backward: in b's place
   __device__ __forceinline__ Vec get_b(int v) const { Vec t; load_vec(t, at[v]); return t; }
   __device__ __forceinline__ Vec get_g(int v) const { Vec t; load_vec(t, at[v] + D); return t; }
 };
@@ -350,6 +371,7 @@ __device__ __forceinline__ void load_coefficients(const NormArgs& p, int g, cons
       for (int i = 0; i < 4; ++i) a.v[i] = mul2(a.v[i], t.v[i]);
     }
     k.a[v] = a;
+    if (SHARED && !want_b) k.put(0, v, a);
     fill(o, 1.f);
     if (p.gate) load_vec(o, p.gate + at);
     if (p.post_weight) {
@@ -369,7 +391,7 @@ template <int CLS, bool BACK>
 struct Class {
   static constexpr int kV = CLS == 0 ? 1 : 2;
   static constexpr int kMax = CLS == 0 ? 128 : CLS == 1 ? 128 : CLS == 2 ? 320 : 512;
-  static constexpr int kThreads = CLS == 0 ? (BACK ? 512 : 768) : CLS == 1 ? (BACK ? 384 : 640) : CLS == 2 ? (BACK ? 320 : 640) : 512;
+  static constexpr int kThreads = CLS == 0 ? (BACK ? 512 : 768) : CLS == 1 ? (BACK ? 512 : 640) : CLS == 2 ? (BACK ? 320 : 640) : 512;
 };
 
 // Shared memory of the wide rows: the ring's stages, then two coefficients per column.
@@ -378,39 +400,38 @@ __device__ __forceinline__ uint8_t* coefficient_memory(const NormArgs& p) {
   return dyn + p.ring_bytes;
 }
 
+template <int CLS>
+using Sum = RowSum<CLS == 0 ? -1 : CLS == 1 ? 2 : 4>;  // up to 4, 10 and 16 warps
+
 template <typename TX, typename TY, int CLS>
 __global__ void __launch_bounds__(Class<CLS, false>::kMax, (Class<CLS, false>::kThreads / Class<CLS, false>::kMax))
     k_block_norm(const __grid_constant__ NormArgs p) {
   constexpr int V = Class<CLS, false>::kV;
   __shared__ float2 scratch[64];
-  RowSum sum(scratch, p.tpr);
+  Sum<CLS> sum(scratch, p.tpr);
   const Place pl = place(p);
   Columns<V> c;
   c.init(p.D, p.tpr, pl.lane, sum);
   typename std::conditional<CLS == 0, Direct<TX, TY, 2, V>, Ring<TX, TY, 2, V>>::type rows(p, c, pl.row, pl.end);
-  int g = pl.row < pl.end ? group_of(p, (int)pl.row) : 0;
-  long long gend = pl.row;  // the first row loads the coefficients
+  int g = pl.row < pl.end ? group_of(p, pl.row) : 0;
+  int gend = pl.row;  // the first row loads the coefficients
   // a sum over the block is the barrier behind which a stage is free
   const bool barrier = (p.y && p.post != SVGEAR_NORM_NONE) || (p.h && p.pre != SVGEAR_NORM_NONE);
   Coefficients<V, CLS != 0> k(p, c, coefficient_memory(p));
-  TX* r_out = static_cast<TX*>(p.r) + pl.row * p.D;
-  TY* h_out = static_cast<TY*>(p.h) + pl.row * p.D;
-  for (int it = 0; it < p.chunk; ++it, r_out += p.D, h_out += p.D) {
-    const long long row = pl.row + it;
+  for (int it = 0; it < p.chunk; ++it) {
+    const int row = pl.row + it;
     const bool live = row < pl.end;
     if (p.tpr >= 32 && !live) break;  // uniform over the worker, which is whole warps
     if (live && row >= gend) {
       while ((gend = group_end(p, g)) <= row && g + 1 < p.G) ++g;
       load_coefficients(p, g, c, k, true);
     }
-    Row<TX, TY, V> in;
-    rows.take(row, in);
+    rows.take(row);
+    const long long out = (long long)row * p.D;
     Vec f[V], m[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) unpack(in.x[v], f[v]);
+    rows.template read<kX>(f);
     if (p.y) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) unpack(in.y[v], m[v]);
+      rows.template read<kY>(m);
       normalise<V>(m, c, p.post, p.eps, sum);
       const f2 a = pair(p.a);
 #pragma unroll
@@ -418,7 +439,7 @@ __global__ void __launch_bounds__(Class<CLS, false>::kMax, (Class<CLS, false>::k
         const Vec cg = k.get_g(v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[v].v[i] = fma2(a, f[v].v[i], mul2(cg.v[i], m[v].v[i]));
-        if (live && c.on[v]) store_vec(r_out + c.col[v], f[v]);
+        if (live && c.on[v]) store_vec(static_cast<TX*>(p.r) + out + c.col[v], f[v]);
       }
     }
     if (p.h) {
@@ -429,7 +450,7 @@ __global__ void __launch_bounds__(Class<CLS, false>::kMax, (Class<CLS, false>::k
         const Vec cb = k.get_b(v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[v].v[i] = fma2(mul2(add2(f[v].v[i], mean), inv), k.a[v].v[i], cb.v[i]);
-        if (live && c.on[v]) store_vec(h_out + c.col[v], f[v]);
+        if (live && c.on[v]) store_vec(static_cast<TY*>(p.h) + out + c.col[v], f[v]);
       }
     }
     if (CLS != 0 && !barrier) __syncthreads();
@@ -439,8 +460,8 @@ __global__ void __launch_bounds__(Class<CLS, false>::kMax, (Class<CLS, false>::k
 
 // du -> the gradient of the norm's input: inv (du - n mean(du n) - mean(du)),
 // the last term for a layer norm only.  n is the normalised row.
-template <int V>
-__device__ __forceinline__ void norm_back(Vec (&du)[V], const Vec (&n)[V], const Columns<V>& c, float inv, int kind, RowSum& sum) {
+template <int V, typename SUM>
+__device__ __forceinline__ void norm_back(Vec (&du)[V], const Vec (&n)[V], const Columns<V>& c, float inv, int kind, SUM& sum) {
   if (kind == SVGEAR_NORM_NONE) return;
   float2 s = make_float2(0.f, 0.f);
 #pragma unroll
@@ -469,19 +490,16 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
     k_block_norm_back(const __grid_constant__ NormArgs p) {
   constexpr int V = Class<CLS, true>::kV;
   __shared__ float2 scratch[64];
-  RowSum sum(scratch, p.tpr);
+  Sum<CLS> sum(scratch, p.tpr);
   const Place pl = place(p);
   Columns<V> c;
   c.init(p.D, p.tpr, pl.lane, sum);
   typename std::conditional<CLS == 0, Direct<TX, TY, 4, V>, Ring<TX, TY, 4, V>>::type rows(p, c, pl.row, pl.end);
-  int g = pl.row < pl.end ? group_of(p, (int)pl.row) : 0;
-  long long gend = pl.row;
-  const bool barrier = (p.y && p.post != SVGEAR_NORM_NONE) || (p.dh && p.pre != SVGEAR_NORM_NONE);
+  int g = pl.row < pl.end ? group_of(p, pl.row) : 0;
+  int gend = pl.row;
   const f2 a = pair(p.y ? p.a : 1.f);
   Coefficients<V, CLS != 0> k(p, c, coefficient_memory(p));
   Vec s1[V], s2[V], su[V];
-  TX* dx_out = static_cast<TX*>(p.dx) + pl.row * p.D;
-  TY* dy_out = static_cast<TY*>(p.dy) + pl.row * p.D;
   auto flush = [&]() {
     float* part = p.part + (size_t)(pl.worker + g) * 3 * p.D;
 #pragma unroll
@@ -492,8 +510,8 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
         store_vec(part + 2 * p.D + c.col[v], su[v]);
       }
   };
-  for (int it = 0; it < p.chunk; ++it, dx_out += p.D, dy_out += p.D) {
-    const long long row = pl.row + it;
+  for (int it = 0; it < p.chunk; ++it) {
+    const int row = pl.row + it;
     const bool live = row < pl.end;
     if (p.tpr >= 32 && !live) break;
     if (live && row >= gend) {
@@ -507,70 +525,75 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
         fill(su[v], 0.f);
       }
     }
-    Row<TX, TY, V> in;
-    rows.take(row, in);
-    Vec n[V], m[V], R[V];
-    float inv_m = 1.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      unpack(in.x[v], n[v]);
-      unpack(in.dh[v], R[v]);
-    }
+    rows.take(row);
+    const long long out = (long long)row * p.D;
+    Vec n[V], R[V];
+    float2 st_m = make_float2(0.f, 1.f);  // mean and 1/deviation of y
+    rows.template read<kX>(n);
     if (p.y) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) unpack(in.y[v], m[v]);
-      inv_m = normalise<V>(m, c, p.post, p.eps, sum);
+      rows.template read<kY>(R);
+      if (p.post != SVGEAR_NORM_NONE) {
+        st_m = statistics<V>(R, c, p.post, p.eps, sum);
+        apply<V>(R, st_m);
+      }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const Vec cg = k.get_g(v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) n[v].v[i] = fma2(a, n[v].v[i], mul2(cg.v[i], m[v].v[i]));
+        for (int i = 0; i < 4; ++i) n[v].v[i] = fma2(a, n[v].v[i], mul2(cg.v[i], R[v].v[i]));
       }
     }
     if (p.dh) {
       const float inv_n = normalise<V>(n, c, p.pre, p.eps, sum);
+      rows.template read<kDh>(R);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v) {
+        const Vec ca = k.get_a(v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (CLS != 0 || live) {
             s1[v].v[i] = add2(s1[v].v[i], R[v].v[i]);
             s2[v].v[i] = fma2(R[v].v[i], n[v].v[i], s2[v].v[i]);
           }
-          R[v].v[i] = mul2(R[v].v[i], k.a[v].v[i]);
+          R[v].v[i] = mul2(R[v].v[i], ca.v[i]);
         }
+      }
       norm_back<V>(R, n, c, inv_n, p.pre, sum);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) fill(R[v], 0.f);
     }
     if (p.dr) {
+      rows.template read<kDr>(n);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        unpack(in.dr[v], n[v]);
+      for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < 4; ++i) R[v].v[i] = add2(R[v].v[i], n[v].v[i]);
-      }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) n[v].v[i] = mul2(a, R[v].v[i]);
-      if (live && c.on[v]) store_vec(dx_out + c.col[v], n[v]);
+      if (live && c.on[v]) store_vec(static_cast<TX*>(p.dx) + out + c.col[v], n[v]);
     }
     if (p.y) {
+      rows.template read<kY>(n);  // again: kept in registers it would cost the fourth block per SM
+      if (p.post != SVGEAR_NORM_NONE) apply<V>(n, st_m);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const Vec cg = k.get_g(v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (CLS != 0 || live) su[v].v[i] = fma2(R[v].v[i], m[v].v[i], su[v].v[i]);
+          if (CLS != 0 || live) su[v].v[i] = fma2(R[v].v[i], n[v].v[i], su[v].v[i]);
           R[v].v[i] = mul2(R[v].v[i], cg.v[i]);
         }
       }
-      norm_back<V>(R, m, c, inv_m, p.post, sum);
+      norm_back<V>(R, n, c, st_m.y, p.post, sum);
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (live && c.on[v]) store_vec(dy_out + c.col[v], R[v]);
+        if (live && c.on[v]) store_vec(static_cast<TY*>(p.dy) + out + c.col[v], R[v]);
     }
-    if (CLS != 0 && !barrier) __syncthreads();
+    if (CLS != 0) __syncthreads();  // the row has been read
     rows.release(row);
   }
   if (pl.row < pl.end) flush();

@@ -159,7 +159,7 @@ __device__ __forceinline__ float dot(const Sixteen& x, const Sixteen& y) {
 struct Place {
   int slot, lane, lanes, j, head, off;  // off: element offset of the low vector in a token
   bool on;
-  long long t, end;                     // tokens [t, end), counted b * N + n
+  int t, end;                           // tokens [t, end), counted b * N + n
 };
 __device__ __forceinline__ Place place(const RopeArgs& p) {
   Place q;
@@ -170,16 +170,16 @@ __device__ __forceinline__ Place place(const RopeArgs& p) {
   q.j = q.lane - q.head * q.lanes;
   q.on = q.head < p.H;
   q.off = q.head * p.d + q.j * kVec;
-  const long long total = (long long)p.B * p.N;
-  q.t = ((long long)blockIdx.x * (blockDim.x / p.tpt) + q.slot) * p.chunk;
-  q.end = q.t + p.chunk < total ? q.t + p.chunk : total;
+  const long long total = (long long)p.B * p.N, first = ((long long)blockIdx.x * (blockDim.x / p.tpt) + q.slot) * p.chunk;
+  q.t = (int)min(first, total);
+  q.end = (int)min(first + p.chunk, total);
   return q;
 }
 
 // Batch entry and token, stepped without divisions.
 struct Token {
   int b, n;
-  __device__ __forceinline__ Token(const RopeArgs& p, long long t) : b((int)(t / p.N)), n((int)(t - (long long)(t / p.N) * p.N)) {}
+  __device__ __forceinline__ Token(const RopeArgs& p, int t) : b(t / p.N), n(t - t / p.N * p.N) {}
   __device__ __forceinline__ void step(int N) {
     if (++n == N) { n = 0; ++b; }
   }
@@ -305,7 +305,7 @@ struct Direct {
   const RopeArgs& p;
   const Place& pl;
   Token ahead;
-  long long t;
+  int t;
   Raw<T> nx[OPS][2];
   __device__ __forceinline__ void load() {
 #pragma unroll
@@ -340,7 +340,7 @@ struct Ring {
   const RopeArgs& p;
   const Place& pl;
   Token ahead;       // the next token to be copied
-  long long t;
+  int t;
   uint32_t row;      // bytes of a token's row
   uint64_t* full;
   volatile int* abort_flag;
@@ -382,14 +382,16 @@ struct Ring {
     for (int k = 0; k < OPS; ++k) any |= p.in[k] != nullptr;
     // A wait that gives up records it; the block goes on with what is there, so every thread still meets every barrier.
     if (any) tc::mbar_wait(full + slot, parity, abort_flag, p.status);
-    const uint8_t* at = shared_base() + slot * OPS * row + pl.off * sizeof(T);
+    // threads without an element read the first ones: they add to no sum and store nothing
+    const uint8_t* at = shared_base() + slot * OPS * row + (pl.on ? pl.off : 0) * sizeof(T);
 #pragma unroll
     for (int k = 0; k < OPS; ++k) {
-      zero_raw(r[k][0]);
-      zero_raw(r[k][1]);
-      if (p.in[k] && pl.on) {
+      if (p.in[k]) {
         r[k][0] = *reinterpret_cast<const Raw<T>*>(at + k * row);
         r[k][1] = *reinterpret_cast<const Raw<T>*>(at + k * row + p.d / 2 * sizeof(T));
+      } else {
+        zero_raw(r[k][0]);
+        zero_raw(r[k][1]);
       }
     }
   }
@@ -428,7 +430,7 @@ struct Gradients {
   const RopeArgs& p;
   const Place& pl;
   Token ahead;
-  long long t;
+  int t;
   uint32_t at;
   int slot;
   uint8_t* mem;
@@ -486,7 +488,7 @@ template <typename T, bool HALF, int CLS>
 __global__ void __launch_bounds__(Class<CLS, false>::kMax, (Class<CLS, false>::kThreads / Class<CLS, false>::kMax))
     k_qkv_rope(const __grid_constant__ RopeArgs p) {
   __shared__ float2 scratch[64];
-  RowSum sum(scratch, p.tpt);
+  RowSum<CLS == 0 ? -1 : CLS == 1 ? 2 : CLS == 2 ? 4 : 5> sum(scratch, p.tpt);
   const Place pl = place(p);
   const int half = p.d / 2;
   const float inv_c = 1.f / (float)(p.norm == SVGEAR_QKNORM_TOKEN ? p.H * p.d : p.d);
@@ -513,6 +515,7 @@ __global__ void __launch_bounds__(Class<CLS, false>::kMax, (Class<CLS, false>::k
     for (int k = 0; k < 2; ++k) spread<HALF>(raw[k][0], raw[k][1], z[k]);
     if (p.norm != SVGEAR_QKNORM_NONE) {
       float2 s = make_float2(dot(z[0], z[0]), dot(z[1], z[1]));
+      if (!pl.on) s = make_float2(0.f, 0.f);
       if (p.norm == SVGEAR_QKNORM_TOKEN) {
         s = sum(s);
       } else {
@@ -553,7 +556,7 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
     k_qkv_rope_back(const __grid_constant__ RopeArgs p) {
   __shared__ float2 scratch[128];
   constexpr bool kAhead = ahead_of<T>(CLS);
-  RowSum sum(scratch, p.tpt);
+  RowSum<CLS == 0 ? -1 : CLS == 1 ? 2 : CLS == 2 ? 4 : 5> sum(scratch, p.tpt);
   const Place pl = place(p);
   const int half = p.d / 2;
   const float inv_c = 1.f / (float)(p.norm == SVGEAR_QKNORM_TOKEN ? p.H * p.d : p.d);
@@ -602,6 +605,7 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
         Sixteen u = z[k];
         w.apply(k, u);
         s[k] = make_float2(dot(x[k], x[k]), dot(u, x[k]));
+        if (!pl.on) s[k] = make_float2(0.f, 0.f);
       }
       if (p.norm == SVGEAR_QKNORM_TOKEN) {
         sum.both(s[0], s[1]);
@@ -640,7 +644,7 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
   }
   if (!p.part) return;
   const long long worker = (long long)blockIdx.x * (blockDim.x / p.tpt) + pl.slot;
-  const bool has = pl.t < (long long)p.B * p.N;  // workers without a token have no slot
+  const bool has = pl.t < pl.end;  // workers without a token have no slot
   if (p.norm == SVGEAR_QKNORM_TOKEN) {
     if (has && pl.on)
 #pragma unroll

@@ -134,70 +134,70 @@ __device__ __forceinline__ void fill(Vec& f, float x) {
   for (int i = 0; i < 4; ++i) f.v[i] = pair(x);
 }
 
-// Sums over the `width` lanes of a worker: 4, 8, 16 or 32 lanes of a warp, or a
-// whole block of up to 32 warps.  Every thread of the block calls it the same
-// number of times; `scratch` ([2][32]) alternates between two halves, so one
-// barrier per sum suffices: a half is written again only behind the next
-// sum's barrier, which every reader of it has reached.
+// Sums over the lanes of a worker.  STEPS < 0: `width` = 4, 8, 16 or 32 lanes of
+// a warp.  Otherwise a whole block of `width` / 32 <= 2^STEPS warps; every
+// thread of the block calls it the same number of times.  `scratch` ([2][32], for
+// `both` [4][32]) alternates between two halves, so one barrier per sum
+// suffices: a half is written again only behind the next sum's barrier, which
+// every reader of it has reached.
+template <int STEPS>
 struct RowSum {
+  static constexpr bool kBlock = STEPS >= 0;
+  static constexpr int kMask = kBlock ? (1 << STEPS) - 1 : 0;
   float2* scratch;
-  int width, phase, top, mask;  // top, mask: the tree over the warps' totals
-  __device__ __forceinline__ RowSum(float2* s, int w) : scratch(s), width(w), phase(0), top(0), mask(0) {
-    if (w > 32) {
-      for (top = 1; top < w >> 5; top <<= 1) {}
-      mask = top - 1;
-      top >>= 1;
-    }
-  }
-  __device__ __forceinline__ float2 lanes(float2 v) const {
-    for (int o = (width < 32 ? width : 32) >> 1; o > 0; o >>= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
-    return v;
-  }
+  int width, phase;
+  __device__ __forceinline__ RowSum(float2* s, int w) : scratch(s), width(w), phase(0) {}
   __device__ __forceinline__ float lanes(float v) const {
-    for (int o = (width < 32 ? width : 32) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (kBlock) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    } else {
+      for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
     return v;
   }
-  // Trades the warps' values: lane i gets warp (i & mask)'s, zeros behind the last warp.
+  __device__ __forceinline__ float2 lanes(float2 v) const { return make_float2(lanes(v.x), lanes(v.y)); }
+  __device__ __forceinline__ float2 other(const float2* s) const {
+    const int i = threadIdx.x & kMask;
+    return i < width >> 5 ? s[i] : make_float2(0.f, 0.f);
+  }
+  // Trades the warps' values: lane i gets warp (i & kMask)'s, zeros behind the last warp.
   __device__ __forceinline__ float2 trade(float2 v) {
     float2* s = scratch + phase * 32;
     phase ^= 1;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
-    const int i = threadIdx.x & mask;
-    return i < width >> 5 ? s[i] : make_float2(0.f, 0.f);
+    return other(s);
   }
   __device__ __forceinline__ float warps(float v) const {
-    for (int o = top; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+    for (int o = (kMask + 1) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   }
   __device__ __forceinline__ float2 operator()(float2 v) {
     v = lanes(v);
-    if (width > 32) {
+    if (kBlock) {
       v = trade(v);
       v = make_float2(warps(v.x), warps(v.y));
     }
     return v;
   }
-  // Two pairs behind one barrier; `scratch` has two more halves for it ([4][32]).
+  // Two pairs behind one barrier.
   __device__ __forceinline__ void both(float2& a, float2& b) {
     a = lanes(a);
     b = lanes(b);
-    if (width > 32) {
+    if (kBlock) {
       float2* s = scratch + 64 + phase * 32;
       if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = b;
       a = trade(a);
-      const int i = threadIdx.x & mask;
-      b = i < width >> 5 ? s[i] : make_float2(0.f, 0.f);
+      b = other(s);
       a = make_float2(warps(a.x), warps(a.y));
       b = make_float2(warps(b.x), warps(b.y));
     }
   }
   __device__ __forceinline__ float operator()(float v) {
     v = lanes(v);
-    return width > 32 ? warps(trade(make_float2(v, 0.f)).x) : v;
+    return kBlock ? warps(trade(make_float2(v, 0.f)).x) : v;
   }
 };
 

@@ -361,7 +361,8 @@ SVGEAR_API int svgear_forward(const void* Q, const void* K, const void* V, const
  *   y NULL: gate and post_weight NULL, post NONE, res_scale 1, r NULL.
  *   h NULL: only r is formed.
  * r may be x, and h may be y (or x when y is NULL) where the types agree.
- * D a multiple of 8, at most 8192 (else SVGEAR_ERR_UNSUPPORTED); eps > 0.
+ * D a multiple of 8, at most 8192, and N at most 2^30 (else
+ * SVGEAR_ERR_UNSUPPORTED); eps > 0.
  * ------------------------------------------------------------------------- */
 typedef enum { SVGEAR_NORM_NONE = 0, SVGEAR_NORM_RMS = 1, SVGEAR_NORM_LAYER = 2 } svgear_norm;
 
@@ -419,7 +420,7 @@ SVGEAR_API int svgear_block_norm_backward(const void* x, const void* y, const vo
  *     out_tokens 0 means N.  With out_tokens > N the rows behind are left as
  *     they were, and a pointer moved by t*d places the tokens at row t: a
  *     joint sequence is written by one call per part.
- * d in {64, 128}, H*d <= 16384.
+ * d in {64, 128}, H*d <= 16384, B*N <= 2^30 (else SVGEAR_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------- */
 typedef enum { SVGEAR_PAIR_ADJACENT = 0, SVGEAR_PAIR_HALF = 1 } svgear_pairing;
 typedef enum { SVGEAR_QKNORM_NONE = 0, SVGEAR_QKNORM_HEAD = 1, SVGEAR_QKNORM_TOKEN = 2 } svgear_qknorm;

@@ -365,7 +365,8 @@ def test_refusals_of_parameters(L):
     bad = [(dict(N=0), INV), (dict(D=0), INV), (dict(G=0), INV), (dict(N=-1), INV), (dict(pre=3), INV), (dict(post=-1), INV),
            (dict(eps=0.0), INV), (dict(eps=-1.0), INV), (dict(eps=math.nan), INV), (dict(eps=math.inf), INV),
            (dict(res_scale=math.nan), INV), (dict(res_scale=math.inf), INV), (dict(dtype=2), UNS), (dict(res_dtype=-1), UNS),
-           (dict(dtype=sv.SVGEAR_F32), UNS), (dict(D=68), UNS), (dict(D=8200), UNS)]
+           (dict(dtype=sv.SVGEAR_F32), UNS), (dict(D=68), UNS), (dict(D=8200), UNS),
+           (dict(N=2 ** 30 + 4), UNS)]
     for kw, code in bad:
         assert fwd(L, P(**kw)) == code, kw
         assert bwd(L, P(**kw)) == code, kw

@@ -85,23 +85,23 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
                : "memory");
 }
 
-// Scales [8 kb, 8 kb + 8) of a row with `pitch` scales; 0 behind the end.
-__device__ __forceinline__ uint2 load_scales(const uint8_t* row, int pitch, int kb) {
-  uint2 v = make_uint2(0, 0);
-  const uint8_t* s = row + kb * 8;
-  const int left = pitch - kb * 8;
-  if ((pitch & 7) == 0) return __ldg(reinterpret_cast<const uint2*>(s));  // then left >= 8
+// Scales [16 u, 16 u + 16) of a row with `pitch` scales (two stages); 0 behind
+// the end.  As wide as the rows are aligned.
+__device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pitch, int u) {
+  const uint8_t* s = row + u * 16;
+  if ((pitch & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(s));
+  uint32_t v[4] = {0, 0, 0, 0};
+  const int left = pitch - u * 16;
   if ((pitch & 3) == 0) {
-    v.x = __ldg(reinterpret_cast<const uint32_t*>(s));
-    if (left > 4) v.y = __ldg(reinterpret_cast<const uint32_t*>(s) + 1);
-    return v;
-  }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i < left) v.x |= (uint32_t)__ldg(s + i) << (8 * i);
-    if (i + 4 < left) v.y |= (uint32_t)__ldg(s + i + 4) << (8 * i);
+    for (int i = 0; i < 4; ++i)
+      if (4 * i < left) v[i] = __ldg(reinterpret_cast<const uint32_t*>(s) + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < left) v[i >> 2] |= (uint32_t)__ldg(s + i) << (8 * (i & 3));
   }
-  return v;
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 template <int TN>
@@ -214,44 +214,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ scales
-    const int r = threadIdx.x - 128;  // row 0..127 of the features, and rows r, r + 128 of the tokens
-    const int pitch = p.K / 32;
+    // Row r of the features and rows r, r + 128 of the tokens.  A load takes the
+    // scales of two stages and runs two loads (two to four stages) ahead of
+    // the stores, over tile boundaries too.
+    const int r = threadIdx.x - 128;
+    const int pitch = p.K / 32, units = (p.kblocks + 1) / 2;
     constexpr int R = T::kTokBlocks;
-    uint32_t it = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
-      const int f = t % p.ftiles * kTF + r, m0 = t / p.ftiles * TN;
-      const uint8_t* rows[R + 1];
-      rows[0] = f < p.N ? p.w_scales + (size_t)f * pitch : nullptr;
+    struct Unit {
+      uint4 v[R + 1];
+    };
+    int ft = blockIdx.x, fu = 0;  // the next unit to load
+    auto fetch = [&](Unit& x) {
+      const int f = ft % p.ftiles * kTF + r, m0 = ft / p.ftiles * TN;
+      const bool more = ft < p.tiles;
+      x.v[0] = more && f < p.N ? load_scales(p.w_scales + (size_t)f * pitch, pitch, fu) : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int b = 0; b < R; ++b) {
         const int m = r + b * 128;
-        rows[b + 1] = m < TN && m0 + m < p.M ? p.a_scales + (size_t)(m0 + m) * pitch : nullptr;
+        x.v[b + 1] = more && m < TN && m0 + m < p.M ? load_scales(p.a_scales + (size_t)(m0 + m) * pitch, pitch, fu) : make_uint4(0, 0, 0, 0);
       }
-      uint2 v[R + 1];
-      auto fetch = [&](int kb) {
-#pragma unroll
-        for (int b = 0; b <= R; ++b) v[b] = rows[b] && kb < p.kblocks ? load_scales(rows[b], pitch, kb) : make_uint2(0, 0);
-      };
-      fetch(0);
-      for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-        const int s = it % S;
-        ok = tc::mbar_wait_warp(empty + s, (it / S & 1) ^ 1, abort_flag, p.status);
-        if (!ok) break;
-        uint8_t* sf = sf_s + s * (T::kSfF + T::kSfT) + (r & 31) * 16 + (r >> 5) * 4;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          *reinterpret_cast<uint32_t*>(sf + i * 512) = i ? v[0].y : v[0].x;
-#pragma unroll
-          for (int b = 0; b < R; ++b)
-            *reinterpret_cast<uint32_t*>(sf + T::kSfF + (i * R + b) * 512) = i ? v[b + 1].y : v[b + 1].x;
-        }
-        fetch(kb + 1);
-        tc::fence_proxy_async();  // the tensor core's copies read what this thread stored
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(sf_full + s);
+      if (++fu == units) {
+        fu = 0;
+        ft += gridDim.x;
       }
-    }
+    };
+    uint32_t it = 0;
+    bool ok = true;
+    auto store = [&](const Unit& x, int h) {
+      const int s = it % S;
+      ok = tc::mbar_wait_warp(empty + s, (it / S & 1) ^ 1, abort_flag, p.status);
+      if (!ok) return;
+      uint8_t* sf = sf_s + s * (T::kSfF + T::kSfT) + (r & 31) * 16 + (r >> 5) * 4;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        *reinterpret_cast<uint32_t*>(sf + i * 512) = h ? (i ? x.v[0].w : x.v[0].z) : (i ? x.v[0].y : x.v[0].x);
+#pragma unroll
+        for (int b = 0; b < R; ++b)
+          *reinterpret_cast<uint32_t*>(sf + T::kSfF + (i * R + b) * 512) =
+              h ? (i ? x.v[b + 1].w : x.v[b + 1].z) : (i ? x.v[b + 1].y : x.v[b + 1].x);
+      }
+      tc::fence_proxy_async();  // the tensor core's copies read what this thread stored
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(sf_full + s);
+      ++it;
+    };
+    Unit x0, x1, x2;
+    fetch(x0);
+    fetch(x1);
+    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x)
+      for (int u = 0; ok && u < units; ++u) {
+        fetch(x2);
+        store(x0, 0);
+        if (ok && 2 * u + 1 < p.kblocks) store(x0, 1);
+        x0 = x1;
+        x1 = x2;
+      }
   } else if (warp >= 8) {
     // ---------------------------------------------------------- epilogue
     const int quarter = warp & 3, f = quarter * 32 + lane, tid = threadIdx.x - 256;

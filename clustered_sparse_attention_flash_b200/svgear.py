@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from typing import Dict, Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -428,76 +429,91 @@ def forward(Q, K, V, Cq: int, Ck: int, iters: int, rho: float, scale: float = 0.
 # These helpers run on the device their tensors are on, whatever device is
 # current, and on `stream` (default: that device's current stream).  Outputs
 # and workspaces are allocated on the same stream, so the caching allocator
-# never hands their memory to work the kernels are not ordered with.
+# never hands their memory to work the kernels are not ordered with.  They
+# check every tensor themselves and call the library with plain pointers: on
+# small inputs the host's time is the call's time.
+
 
 class _On:
-    """Makes `device` current, and `stream` its current stream when one is given."""
-    __slots__ = ("ctx",)
+    """Makes `device` current, and `stream` its current stream when one is given; enters as the stream's handle."""
+    __slots__ = ("device", "ctx")
 
     def __init__(self, device, stream):
         import torch
-        self.ctx = []
-        if device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(device))
+        self.device = device.index
+        self.ctx = None
+        if self.device != torch.cuda.current_device():
+            self.ctx = [torch.cuda.device(device)]
         if stream is not None:
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-            self.ctx.append(torch.cuda.stream(stream))
+            self.ctx = (self.ctx or []) + [torch.cuda.stream(stream)]
 
     def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
+        import torch
+        if self.ctx:
+            for c in self.ctx:
+                c.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.device)
 
     def __exit__(self, *e):
-        for c in reversed(self.ctx):
-            c.__exit__(*e)
+        if self.ctx:
+            for c in reversed(self.ctx):
+                c.__exit__(*e)
 
 
 def _want(name, t, dtype, shape, device, contiguous=True):
-    """Checks one optional tensor argument against what the call expects."""
+    """Checks one optional tensor argument against what the call expects; returns its address."""
     if t is None:
-        return
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name}: a tensor on {device} expected, got {t.device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
+        return None
+    if t.dtype is not dtype or t.device != device or t.shape != shape or (contiguous and not t.is_contiguous()):
+        if t.device != device:
+            raise ValueError(f"{name}: a tensor on {device} expected, got {t.device}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
         raise ValueError(f"{name}: contiguous tensor expected")
+    return t.data_ptr()
+
+
+def _code(dtype) -> int:
+    import torch
+    if dtype is torch.bfloat16:
+        return SVGEAR_BF16
+    if dtype is torch.float32:
+        return SVGEAR_F32
+    raise ValueError(f"unsupported dtype {dtype}")
 
 
 def _norm_call(x, y, dtype, gate, scale, shift, weight, bias, post_weight, pre, post, eps, res_scale, offsets):
-    """Checks the inputs shared by forward and backward; returns the parameter block."""
+    """Checks the inputs shared by forward and backward; returns the parameter block and the addresses of
+    x, y, gate, scale, shift, weight, bias, post_weight and offsets."""
     import torch
     if x.dim() != 2:
         raise ValueError(f"x: [N, D] expected, got shape {tuple(x.shape)}")
-    N, D = x.shape
     if not x.is_cuda:
         raise ValueError("x: device tensor expected")
     if not x.is_contiguous():
         raise ValueError("x: contiguous tensor expected")
+    N, D = x.shape
     dev, f32 = x.device, torch.float32
-    _want("y", y, dtype, (N, D), dev)
     G = 1
     if offsets is not None:
         if offsets.dim() != 1 or offsets.shape[0] < 2:
             raise ValueError("offsets: [G + 1] int32 expected")
         G = offsets.shape[0] - 1
-    else:
-        for t in (gate, scale, shift):
-            if t is not None:
-                G = t.shape[0]
-                break
-    _want("offsets", offsets, torch.int32, (G + 1,), dev)
-    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
-        _want(name, t, f32, (G, D), dev)
-    for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight)):
-        _want(name, t, f32, (D,), dev)
-    codes = {torch.bfloat16: SVGEAR_BF16, torch.float32: SVGEAR_F32}
-    if x.dtype not in codes or dtype not in codes:
-        raise ValueError(f"unsupported dtype {x.dtype if x.dtype not in codes else dtype}")
-    return svgear_norm_params(N, D, G, pre, post, eps, res_scale, codes[dtype], codes[x.dtype])
+    elif gate is not None:
+        G = gate.shape[0]
+    elif scale is not None:
+        G = scale.shape[0]
+    elif shift is not None:
+        G = shift.shape[0]
+    p = svgear_norm_params(N, D, G, pre, post, eps, res_scale, _code(dtype), _code(x.dtype))
+    return p, (x.data_ptr(), _want("y", y, dtype, (N, D), dev), _want("gate", gate, f32, (G, D), dev),
+               _want("scale", scale, f32, (G, D), dev), _want("shift", shift, f32, (G, D), dev),
+               _want("weight", weight, f32, (D,), dev), _want("bias", bias, f32, (D,), dev),
+               _want("post_weight", post_weight, f32, (D,), dev), _want("offsets", offsets, torch.int32, (G + 1,), dev))
 
 
 def block_norm(x, y=None, *, gate=None, scale=None, shift=None, weight=None, bias=None, post_weight=None,
@@ -511,11 +527,12 @@ def block_norm(x, y=None, *, gate=None, scale=None, shift=None, weight=None, bia
     if y is not None and dtype is not None and dtype != y.dtype:
         raise ValueError(f"dtype {dtype} differs from y's {y.dtype}")
     dtype = y.dtype if y is not None else dtype or x.dtype
-    p = _norm_call(x, y, dtype, gate, scale, shift, weight, bias, post_weight, pre, post, eps, res_scale, offsets)
-    with _On(x.device, stream):
+    p, ptrs = _norm_call(x, y, dtype, gate, scale, shift, weight, bias, post_weight, pre, post, eps, res_scale, offsets)
+    with _On(x.device, stream) as st:
         r = torch.empty_like(x) if y is not None else None
         h = torch.empty_like(x, dtype=dtype) if want_h else None
-        svgear_block_norm(x, y, gate, scale, shift, weight, bias, post_weight, offsets, p, r, h)
+        _check("svgear_block_norm", lib().svgear_block_norm(
+            *ptrs, ctypes.byref(p), None if r is None else r.data_ptr(), None if h is None else h.data_ptr(), st))
     return (x if r is None else r), h
 
 
@@ -529,66 +546,70 @@ def block_norm_backward(x, y, dr, dh, *, gate=None, scale=None, shift=None, weig
     if dr is None and dh is None:
         raise ValueError("dr or dh expected")
     dtype = y.dtype if y is not None else dh.dtype if dh is not None else x.dtype
-    p = _norm_call(x, y, dtype, gate, scale, shift, weight, bias, post_weight, pre, post, eps, res_scale, offsets)
-    _want("dr", dr, x.dtype, x.shape, x.device)
-    _want("dh", dh, dtype, x.shape, x.device)
-    like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
-    with _On(x.device, stream):
-        out = {"dx": torch.empty_like(x), "dy": like(y), "dgate": like(gate), "dscale": like(scale),
-               "dshift": like(shift), "dweight": like(weight), "dbias": like(bias),
-               "dpost_weight": like(post_weight)}
-        ws = workspace(svgear_block_norm_backward_workspace_size(p), x.device)
-        svgear_block_norm_backward(x, y, dr, dh, gate, scale, weight, bias, post_weight, offsets, p, out["dx"],
-                                   out["dy"], out["dgate"], out["dscale"], out["dshift"], out["dweight"],
-                                   out["dbias"], out["dpost_weight"], ws, ws.numel())
+    p, ptrs = _norm_call(x, y, dtype, gate, scale, shift, weight, bias, post_weight, pre, post, eps, res_scale, offsets)
+    px, py, pgate, pscale, _, pweight, pbias, ppost, poff = ptrs
+    pdr, pdh = _want("dr", dr, x.dtype, x.shape, x.device), _want("dh", dh, dtype, x.shape, x.device)
+    with _On(x.device, stream) as st:
+        given = {"dx": x, "dy": y, "dgate": gate, "dscale": scale, "dshift": shift, "dweight": weight, "dbias": bias,
+                 "dpost_weight": post_weight}
+        out = {n: None if t is None else torch.empty_like(t) for n, t in given.items()}
+        need = svgear_block_norm_backward_workspace_size(p)
+        ws = workspace(need, x.device)
+        _check("svgear_block_norm_backward", lib().svgear_block_norm_backward(
+            px, py, pdr, pdh, pgate, pscale, pweight, pbias, ppost, poff, ctypes.byref(p),
+            *(None if t is None else t.data_ptr() for t in out.values()), ws.data_ptr(), ws.numel(), st))
     return out
 
 
-def _three(v, kind):
-    return tuple(kind(x) for x in v) if isinstance(v, (tuple, list)) else (kind(v),) * 3
+_ROPE_FMT = struct.Struct("4i9i6f2if3i8q")  # svgear_rope_params, natively aligned
+
+
+def _three(v):
+    return tuple(v) if isinstance(v, (tuple, list)) else (v, v, v)
 
 
 def rope_params(B, N, H, d, axes, grid=(0, 0, 0), origin=0, theta=10000.0, pos_scale=1.0,
                 pairing: int = SVGEAR_PAIR_ADJACENT, norm: int = SVGEAR_QKNORM_NONE, eps: float = 1e-6,
-                dtype: int = SVGEAR_BF16, pos_per_batch: int = 0, out_tokens: int = 0) -> svgear_rope_params:
-    """Parameter block for dense rows [B, N, H, d]; origin, theta and pos_scale are one value or one per axis."""
+                dtype: int = SVGEAR_BF16, pos_per_batch: int = 0, out_tokens: int = 0, ld=None, batch=None,
+                grad_ld=None, grad_batch=None) -> svgear_rope_params:
+    """Parameter block; origin, theta and pos_scale are one value or one per axis, ld and batch the strides of
+    q, k and v (default: dense rows [B, N, H, d], as for the gradients)."""
     if len(axes) != 3 or len(grid) != 3:
         raise ValueError("axes and grid have three entries: time, height, width")
-    I3, F3, L3 = ctypes.c_int * 3, ctypes.c_float * 3, ctypes.c_int64 * 3
-    ld, batch = H * d, N * H * d
-    return svgear_rope_params(B, N, H, d, I3(*axes), I3(*grid), I3(*_three(origin, int)), F3(*_three(theta, float)),
-                              F3(*_three(pos_scale, float)), pairing, norm, eps, dtype, pos_per_batch, out_tokens,
-                              L3(ld, ld, ld), L3(batch, batch, batch), ld, batch)
-
-
-def _rope_rows(name, t, p, i):
-    """Checks the strides of one [B, N, H, d] or [N, H, d] tensor of rows and puts them into p."""
-    if t.stride(-1) != 1 or (p.H > 1 and t.stride(-2) != p.d):
-        raise ValueError(f"{name}: the heads of a token have to be dense")
-    p.ld[i] = t.stride(-3) if p.N > 1 else p.H * p.d
-    p.batch[i] = t.stride(0) if t.dim() == 4 and p.B > 1 else p.N * p.H * p.d
+    row, entry = H * d, N * H * d
+    return svgear_rope_params.from_buffer_copy(_ROPE_FMT.pack(
+        B, N, H, d, *axes, *grid, *_three(origin), *_three(theta), *_three(pos_scale), pairing, norm, eps, dtype,
+        pos_per_batch, out_tokens, *(ld or (row, row, row)), *(batch or (entry, entry, entry)),
+        row if grad_ld is None else grad_ld, entry if grad_batch is None else grad_batch))
 
 
 def _rope_call(rows, wq, wk, axes, grid, positions, origin, theta, pos_scale, pairing, norm, eps, shape, dev, dtype,
-               out_tokens):
+               out_tokens, grad_ld=None, grad_batch=None):
+    """Checks [B, N, H, d] or [N, H, d] rows, weights and positions; returns the parameter block and the
+    addresses of the rows, of wq, wk and of positions."""
     import torch
-    codes = {torch.bfloat16: SVGEAR_BF16, torch.float32: SVGEAR_F32}
-    if dtype not in codes:
-        raise ValueError(f"unsupported dtype {dtype}")
+    code = _code(dtype)
     if len(shape) not in (3, 4):
         raise ValueError(f"rows [B, N, H, d] or [N, H, d] expected, got shape {tuple(shape)}")
     B, (N, H, d) = (shape[0] if len(shape) == 4 else 1), shape[-3:]
-    p = rope_params(B, N, H, d, axes, grid if grid is not None else (0, 0, 0), origin, theta, pos_scale, pairing, norm,
-                    eps, codes[dtype], int(positions is not None and positions.dim() == 3), out_tokens)
-    for i, (name, t) in enumerate(rows):
-        if t is not None:
-            _want(name, t, dtype, shape, dev, contiguous=False)
-            _rope_rows(name, t, p, i)
-    cols = d if norm == SVGEAR_QKNORM_HEAD else H * d
-    _want("wq", wq, torch.float32, (cols,), dev)
-    _want("wk", wk, torch.float32, (cols,), dev)
-    _want("positions", positions, torch.int32, (B, N, 3) if p.pos_per_batch else (N, 3), dev)
-    return p
+    ld, batch, ptrs = [H * d] * 3, [N * H * d] * 3, [None] * 3
+    for i, t in enumerate(rows):
+        if t is None:
+            continue
+        ptrs[i] = _want("qkv"[i], t, dtype, shape, dev, contiguous=False)
+        st = t.stride()
+        if st[-1] != 1 or (H > 1 and st[-2] != d):
+            raise ValueError(f"{'qkv'[i]}: the heads of a token have to be dense")
+        if N > 1:
+            ld[i] = st[-3]
+        if B > 1:
+            batch[i] = st[0]
+    per_batch = int(positions is not None and positions.dim() == 3)
+    cols = (d if norm == SVGEAR_QKNORM_HEAD else H * d,)
+    ptrs += [_want("wq", wq, torch.float32, cols, dev), _want("wk", wk, torch.float32, cols, dev),
+             _want("positions", positions, torch.int32, (B, N, 3) if per_batch else (N, 3), dev)]
+    return rope_params(B, N, H, d, axes, grid or (0, 0, 0), origin, theta, pos_scale, pairing, norm, eps, code,
+                       per_batch, out_tokens, ld, batch, grad_ld, grad_batch), ptrs
 
 
 def qkv_rope(q, k, v, *, axes, grid=None, positions=None, wq=None, wk=None, origin=0, theta=10000.0, pos_scale=1.0,
@@ -599,26 +620,27 @@ def qkv_rope(q, k, v, *, axes, grid=None, positions=None, wq=None, wk=None, orig
     head-major order.  Each of q, k, v may be None.  With out=(Q, K, V), tensors [B*H, M, d], the tokens go to
     rows [out_at, out_at + N) and the others stay (a joint sequence, part by part).  Returns (Q, K, V)."""
     import torch
-    given = [t for t in (q, k, v) if t is not None]
-    if not given:
+    x = q if q is not None else k if k is not None else v
+    if x is None:
         raise ValueError("one of q, k, v expected")
-    x = given[0]
     if not x.is_cuda:
         raise ValueError("device tensor expected")
-    dev = x.device
-    M = x.shape[-3] if out is None else next(t.shape[1] for t in out if t is not None)
-    p = _rope_call((("q", q), ("k", k), ("v", v)), wq, wk, axes, grid, positions, origin, theta, pos_scale, pairing,
-                   norm, eps, x.shape, dev, x.dtype, M)
+    dev, dtype, shape = x.device, x.dtype, x.shape
+    N = shape[-3] if len(shape) >= 3 else 0
+    M = N if out is None else next(t.shape[1] for t in out if t is not None)
+    p, ptrs = _rope_call((q, k, v), wq, wk, axes, grid, positions, origin, theta, pos_scale, pairing, norm, eps, shape,
+                         dev, dtype, M)
     shape = (p.B * p.H, M, p.d)
-    with _On(dev, stream):
+    if not 0 <= out_at <= M - N:
+        raise ValueError(f"out_at {out_at}: {N} tokens do not fit into {M} rows there")
+    with _On(dev, stream) as st:
         if out is None:
-            out = tuple(None if t is None else torch.empty(shape, dtype=x.dtype, device=dev) for t in (q, k, v))
-        if not 0 <= out_at <= M - p.N:
-            raise ValueError(f"out_at {out_at}: {p.N} tokens do not fit into {M} rows there")
-        for name, t in zip(("Q", "K", "V"), out):
-            _want(name, t, x.dtype, shape, dev)
-        dst = [None if t is None else t[:, out_at:] for t in out]
-        svgear_qkv_rope(q, k, v, wq, wk, positions, p, *dst)
+            out = tuple([None if t is None else torch.empty(shape, dtype=dtype, device=dev) for t in (q, k, v)])
+            dst = [None if t is None else t.data_ptr() for t in out]
+        else:
+            at = out_at * p.d * x.element_size()
+            dst = [None if t is None else _want(n, t, dtype, shape, dev) + at for n, t in zip("QKV", out)]
+        _check("svgear_qkv_rope", lib().svgear_qkv_rope(*ptrs, ctypes.byref(p), *dst, st))
     return tuple(out)
 
 
@@ -630,37 +652,42 @@ def qkv_rope_backward(dQ, dK, dV, q=None, k=None, *, axes, grid=None, positions=
     dq, dk and dv are views [B, N, H, d] of one fused buffer [B, N, 3, H, d] ([N, H, d] when q or k has no
     batch).  Returns a dict with dq, dk, dv, dwq, dwk; None for what was not given."""
     import torch
-    given = [t for t in (dQ, dK, dV) if t is not None]
-    if not given:
+    grads = (dQ, dK, dV)
+    have = [i for i in range(3) if grads[i] is not None]
+    if not have:
         raise ValueError("one of dQ, dK, dV expected")
-    g = given[0]
+    g = grads[have[0]]
     if not g.is_cuda or g.dim() != 3:
         raise ValueError("gradients [B*H, N, d] on a device expected")
     ref = q if q is not None else k
     if ref is not None:
-        shape = tuple(ref.shape)
+        shape = ref.shape
     else:
         if not H or g.shape[0] % H:
             raise ValueError("H: the number of heads expected where q and k are not given")
         shape = (g.shape[0] // H, g.shape[1], H, g.shape[2])
     if norm != SVGEAR_QKNORM_NONE and ((dQ is not None and q is None) or (dK is not None and k is None)):
         raise ValueError("q and k expected with a norm")
-    p = _rope_call((("q", q), ("k", k), ("v", None)), wq, wk, axes, grid, positions, origin, theta, pos_scale, pairing,
-                   norm, eps, shape, g.device, g.dtype, 0)
-    for name, t in (("dQ", dQ), ("dK", dK), ("dV", dV)):
-        _want(name, t, g.dtype, (p.B * p.H, p.N, p.d), g.device)
-    have = [i for i, t in enumerate((dQ, dK, dV)) if t is not None]
-    with _On(g.device, stream):
+    width = shape[-2] * shape[-1] if len(shape) >= 3 else 0
+    p, (pq, pk, _, pwq, pwk, ppos) = _rope_call(
+        (q, k, None), wq, wk, axes, grid, positions, origin, theta, pos_scale, pairing, norm, eps, shape, g.device, g.dtype,
+        0, len(have) * width, len(have) * width * shape[-3] if len(shape) >= 3 else 0)
+    ptrs = [_want(n, t, g.dtype, (p.B * p.H, p.N, p.d), g.device) for n, t in zip(("dQ", "dK", "dV"), grads)]
+    with _On(g.device, stream) as st:
         fused = torch.empty((p.B, p.N, len(have), p.H, p.d), dtype=g.dtype, device=g.device)
-        p.grad_ld, p.grad_batch = fused.stride(1), fused.stride(0)
-        rows = [None, None, None]
+        rows, dst = [None] * 3, [None] * 3
         for at, i in enumerate(have):
             rows[i] = fused[:, :, at] if len(shape) == 4 else fused[0, :, at]
-        like = lambda w, t: torch.empty_like(w) if w is not None and t is not None else None  # noqa: E731
-        dwq, dwk = like(wq, dQ), like(wk, dK)
-        ws = workspace(svgear_qkv_rope_backward_workspace_size(p), g.device) if dwq is not None or dwk is not None else None
-        svgear_qkv_rope_backward(dQ, dK, dV, q, k, wq, wk, positions, p, *rows, dwq, dwk, ws,
-                                 ws.numel() if ws is not None else 0)
+            dst[i] = fused.data_ptr() + at * width * fused.element_size()
+        dwq = torch.empty_like(wq) if wq is not None and dQ is not None else None
+        dwk = torch.empty_like(wk) if wk is not None and dK is not None else None
+        ws, need = None, 0
+        if dwq is not None or dwk is not None:
+            need = svgear_qkv_rope_backward_workspace_size(p)
+            ws = workspace(need, g.device)
+        _check("svgear_qkv_rope_backward", lib().svgear_qkv_rope_backward(
+            *ptrs, pq, pk, pwq, pwk, ppos, ctypes.byref(p), *dst, None if dwq is None else dwq.data_ptr(),
+            None if dwk is None else dwk.data_ptr(), None if ws is None else ws.data_ptr(), need, st))
     return {"dq": rows[0], "dk": rows[1], "dv": rows[2], "dwq": dwq, "dwk": dwk}
 
 
@@ -670,43 +697,58 @@ def mx_quantize(x, stream=None):
     import torch
     if not x.is_cuda:
         raise ValueError("x: device tensor expected")
-    if x.dim() not in (2, 3):
+    if x.dim() == 2:
+        (M, K), head_d = x.shape, 0
+    elif x.dim() == 3:
+        H, M, head_d = x.shape
+        K = H * head_d
+    else:
         raise ValueError(f"x: [M, K] or [H, M, d] expected, got shape {tuple(x.shape)}")
-    M, K, head_d = (x.shape[0], x.shape[1], 0) if x.dim() == 2 else (x.shape[1], x.shape[0] * x.shape[2], x.shape[2])
-    with _On(x.device, stream):
-        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
-        svgear_mx_quantize(x, dtype_code(x), M, K, head_d, codes, scales)
+    if not x.is_contiguous():
+        raise ValueError("x: contiguous tensor expected")
+    dev = x.device
+    with _On(dev, stream) as st:
+        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=dev)
+        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
+        _check("svgear_mx_quantize", lib().svgear_mx_quantize(
+            x.data_ptr(), _code(x.dtype), M, K, head_d, codes.data_ptr(), scales.data_ptr(), st))
     return codes, scales
 
 
 def mx_dequantize(codes, scales, dtype=None, stream=None):
     """The values [M, K] of codes and scales in `dtype` (default torch.bfloat16), through svgear_mx_dequantize."""
     import torch
-    M, K = codes.shape[0], codes.shape[1] * 2
-    _want("codes", codes, torch.uint8, (M, K // 2), codes.device)
-    _want("scales", scales, torch.uint8, (M, K // 32), codes.device)
-    with _On(codes.device, stream):
-        y = torch.empty((M, K), dtype=dtype or torch.bfloat16, device=codes.device)
-        svgear_mx_dequantize(codes, scales, M, K, y, dtype_code(y))
+    if not codes.is_cuda:
+        raise ValueError("codes: device tensor expected")
+    if codes.dim() != 2:
+        raise ValueError(f"codes: [M, K/2] expected, got shape {tuple(codes.shape)}")
+    M, K, dev = codes.shape[0], codes.shape[1] * 2, codes.device
+    dtype = dtype or torch.bfloat16
+    pc, ps = _want("codes", codes, torch.uint8, (M, K // 2), dev), _want("scales", scales, torch.uint8, (M, K // 32), dev)
+    with _On(dev, stream) as st:
+        y = torch.empty((M, K), dtype=dtype, device=dev)
+        _check("svgear_mx_dequantize", lib().svgear_mx_dequantize(pc, ps, M, K, y.data_ptr(), _code(dtype), st))
     return y
 
 
 def mx_product(a_codes, a_scales, w_codes, w_scales, bias=None, stream=None):
     """Y [M, N] bfloat16 = A W^T + bias for MXFP4 A [M, K] and W [N, K], through svgear_mx_product."""
     import torch
+    if not a_codes.is_cuda:
+        raise ValueError("a_codes: device tensor expected")
+    if a_codes.dim() != 2 or w_codes.dim() != 2:
+        raise ValueError("a_codes [M, K/2] and w_codes [N, K/2] expected")
     M, N, K = a_codes.shape[0], w_codes.shape[0], w_codes.shape[1] * 2
-    dev = a_codes.device
-    _want("a_codes", a_codes, torch.uint8, (M, K // 2), dev)
-    _want("a_scales", a_scales, torch.uint8, (M, K // 32), dev)
-    _want("w_codes", w_codes, torch.uint8, (N, K // 2), dev)
-    _want("w_scales", w_scales, torch.uint8, (N, K // 32), dev)
-    _want("bias", bias, torch.float32, (N,), dev)
-    with _On(dev, stream):
+    dev, u8 = a_codes.device, torch.uint8
+    ptrs = (_want("a_codes", a_codes, u8, (M, K // 2), dev), _want("a_scales", a_scales, u8, (M, K // 32), dev),
+            _want("w_codes", w_codes, u8, (N, K // 2), dev), _want("w_scales", w_scales, u8, (N, K // 32), dev),
+            _want("bias", bias, torch.float32, (N,), dev))
+    with _On(dev, stream) as st:
         y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        need = svgear_mx_product_workspace_size(M, N, K)
+        need = lib().svgear_mx_product_workspace_size(M, N, K)
         ws = workspace(need, dev) if need else None
-        svgear_mx_product(a_codes, a_scales, w_codes, w_scales, bias, M, N, K, y, ws, need)
+        _check("svgear_mx_product", lib().svgear_mx_product(
+            *ptrs, M, N, K, y.data_ptr(), None if ws is None else ws.data_ptr(), need, st))
     return y
 
 

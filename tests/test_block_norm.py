@@ -248,7 +248,7 @@ def test_rows_behind_the_last_group_are_left_as_they_were():
     p = Problem(60, 1024, cuts=[0, 10, 10, 41], seed=2)
     kw = p.kw()
     x, y = p.x.cuda(), p.y.cuda()
-    P = sv._norm_call(x, y, BF, kw["gate"], kw["scale"], kw["shift"], kw["weight"], kw["bias"], kw["post_weight"],
+    P, _ = sv._norm_call(x, y, BF, kw["gate"], kw["scale"], kw["shift"], kw["weight"], kw["bias"], kw["post_weight"],
                       kw["pre"], kw["post"], p.eps, p.a, kw["offsets"])
     r, h, dx, dy = (torch.full_like(x, 7.0) for _ in range(4))
     par = (kw["gate"], kw["scale"], kw["shift"], kw["weight"], kw["bias"], kw["post_weight"], kw["offsets"])
@@ -285,7 +285,7 @@ def test_residual_only_and_in_place():
     r, h = sv.block_norm(x, y, **kw)
     r2, none = sv.block_norm(x, y, want_h=False, **kw)
     assert none is None and torch.equal(r, r2)
-    P = sv._norm_call(x, y, BF, *(kw[n] for n in ("gate", "scale", "shift", "weight", "bias", "post_weight", "pre",
+    P, _ = sv._norm_call(x, y, BF, *(kw[n] for n in ("gate", "scale", "shift", "weight", "bias", "post_weight", "pre",
                                                    "post", "eps", "res_scale", "offsets")))
     sv.svgear_block_norm(x, y, *(kw[n] for n in ("gate", "scale", "shift", "weight", "bias", "post_weight", "offsets")),
                          P, x, y)

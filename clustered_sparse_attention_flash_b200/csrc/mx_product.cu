@@ -321,6 +321,290 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ------------------------------------------------------------- few tokens
+//
+// Up to 64 tokens the product is a stream of the weights.  A cluster of C blocks
+// shares a tile of 128 features: block r takes the r-th part of K, and the
+// partial sums meet through distributed shared memory, added in rank order (no
+// workspace, no atomics, the same bits every time).  C grows while the blocks
+// stay at about one per SM and each has two stages: a second wave costs more
+// than the split gains (us, one token, K = 5,120, C = 1 / 2 / 4 / 8: N = 5,120
+// 11.3 / 8.7 / 8.7 / 12.2; N = 15,360 12.2 / 12.6 / 16.6 / 25.5).
+
+constexpr int kFewThreads = 256;  // warp 0 TMA, 1 MMA, 4-7 scales, then the sums
+
+template <int TN>
+struct FewTile {
+  static constexpr int kCodesF = kTF * 128, kCodesT = TN * 128;
+  static constexpr int kCodes = kCodesF + kCodesT, kSf = 2048;  // 2 atoms each of features and tokens
+  static constexpr int kStages = TN > 16 ? 4 : 5;
+  static constexpr int kBars = 256;
+  static constexpr int kSmem = kStages * (kCodes + kSf) + kBars + 1024;
+  static constexpr int kSfCols = 16;
+  static constexpr int kAlloc = TN + kStages * kSfCols <= 128 ? 128 : 256;
+  static_assert(kStages * kCodes >= TN * kTF * 4, "partial sums take the ring's place");
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of every block of the cluster (warps converged).
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_address(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 load_peer(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Scales [8 kb, 8 kb + 8) of a row with `pitch` scales (one stage); 0 behind the end.
+__device__ __forceinline__ uint2 load_scales8(const uint8_t* row, int pitch, int kb) {
+  const uint8_t* s = row + kb * 8;
+  if ((pitch & 7) == 0) return __ldg(reinterpret_cast<const uint2*>(s));
+  const int left = pitch - kb * 8;
+  uint32_t v[2] = {0, 0};
+  if ((pitch & 3) == 0) {
+    v[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
+    if (left > 4) v[1] = __ldg(reinterpret_cast<const uint32_t*>(s) + 1);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) v[i >> 2] |= (uint32_t)__ldg(s + i) << (8 * (i & 3));
+  }
+  return make_uint2(v[0], v[1]);
+}
+
+template <int TN>
+__global__ void __launch_bounds__(kFewThreads, 2)
+    k_mx_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, const ProductArgs p, int C) {
+  using T = FewTile<TN>;
+  constexpr int S = T::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* codes_s = smem;
+  uint8_t* sf_s = smem + S * T::kCodes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sf_s + S * T::kSf);
+  uint64_t* codes_full = bars;     // [S]
+  uint64_t* sf_full = bars + S;    // [S]
+  uint64_t* empty = bars + 2 * S;  // [S]
+  uint64_t* done = bars + 3 * S;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 3 * S + 2);
+  volatile int* no_flag = abort_flag + 1;  // stays 0: waits that an abort must not cut short
+  static_assert((3 * S + 3) * 8 <= T::kBars, "barrier area");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = C > 1 ? (int)cluster_rank() : 0, tile = blockIdx.x / C;
+  const int f0 = tile % p.ftiles * kTF, m0 = tile / p.ftiles * TN;
+  const int kb0 = (int)((long long)rank * p.kblocks / C), kb1 = (int)((long long)(rank + 1) * p.kblocks / C);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      tc::mbar_init(codes_full + i, 1);
+      tc::mbar_init(sf_full + i, 4);
+      tc::mbar_init(empty + i, 1);
+    }
+    tc::mbar_init(done, 1);
+    *abort_flag = 0;
+    *no_flag = 0;
+    tc::mbar_fence_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(tmem_slot, T::kAlloc);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------- code tiles
+    if (lane == 0) {
+      int it = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const int s = it % S;
+        if (!tc::mbar_wait(empty + s, (it / S & 1) ^ 1, abort_flag, p.status)) break;
+        const uint32_t dst = tc::smem_u32(codes_s + s * T::kCodes);
+        tc::mbar_arrive_expect_tx(codes_full + s, T::kCodes);
+        tc::tma_load_3d(dst, &map_w, kb * (kKB / 2), f0, 0, codes_full + s);
+        tc::tma_load_3d(dst + T::kCodesF, &map_a, kb * (kKB / 2), m0, 0, codes_full + s);
+      }
+      // The block's memory outlives its copies, also after an abort.
+      for (int i = max(it - S, 0); i < it; ++i) tc::mbar_wait(codes_full + i % S, i / S & 1, no_flag, p.status);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- MMAs
+    const bool leader = tc::elect_one();
+    int it = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+      const int s = it % S;
+      if (!(tc::mbar_wait_warp(codes_full + s, it / S & 1, abort_flag, p.status) &&
+            tc::mbar_wait_warp(sf_full + s, it / S & 1, abort_flag, p.status)))
+        break;
+      tc::tc_fence_after();
+      const uint32_t wf = tc::smem_u32(codes_s + s * T::kCodes), tk = wf + T::kCodesF;
+      const uint32_t sf = tc::smem_u32(sf_s + s * T::kSf);
+      const uint32_t tf = tmem + TN + s * T::kSfCols;
+      if (leader) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) copy_scales(tf + i * 4, sf + i * 512);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_mxf4(tmem, tc::desc_kmajor(wf, 0, k), tc::desc_kmajor(tk, 0, k), idesc_mxf4(TN, (k & 1) * 2), tf + (k >> 1) * 4,
+                   tf + 8 + (k >> 1) * 4, (it | k) ? 1u : 0u);
+        tc::mma_commit(empty + s);
+      }
+      __syncwarp();
+    }
+    if (leader) tc::mma_commit(done);
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ scales
+    // Row r of the features and of the tokens, four stages loaded ahead.
+    const int r = threadIdx.x - 128, pitch = p.K / 32;
+    const uint8_t* wrow = f0 + r < p.N ? p.w_scales + (size_t)(f0 + r) * pitch : nullptr;
+    const uint8_t* arow = r < TN && m0 + r < p.M ? p.a_scales + (size_t)(m0 + r) * pitch : nullptr;
+    constexpr int B = 4;
+    uint2 cw[B], ca[B], nw[B], na[B];
+    auto fetch = [&](int kb, uint2 (&w)[B], uint2 (&a)[B]) {
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        w[i] = wrow && kb + i < kb1 ? load_scales8(wrow, pitch, kb + i) : make_uint2(0, 0);
+        a[i] = arow && kb + i < kb1 ? load_scales8(arow, pitch, kb + i) : make_uint2(0, 0);
+      }
+    };
+    fetch(kb0, cw, ca);
+    bool ok = true;
+    for (int kb = kb0; ok && kb < kb1; kb += B) {
+      fetch(kb + B, nw, na);
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        if (!ok || kb + i >= kb1) break;
+        const int it = kb + i - kb0, s = it % S;
+        ok = tc::mbar_wait_warp(empty + s, (it / S & 1) ^ 1, abort_flag, p.status);
+        if (!ok) break;
+        uint8_t* sf = sf_s + s * T::kSf + (r & 31) * 16 + (r >> 5) * 4;
+        *reinterpret_cast<uint32_t*>(sf) = cw[i].x;
+        *reinterpret_cast<uint32_t*>(sf + 512) = cw[i].y;
+        *reinterpret_cast<uint32_t*>(sf + 1024) = ca[i].x;
+        *reinterpret_cast<uint32_t*>(sf + 1536) = ca[i].y;
+        tc::fence_proxy_async();  // the tensor core's copies read what this thread stored
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(sf_full + s);
+      }
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        cw[i] = nw[i];
+        ca[i] = na[i];
+      }
+    }
+    // -------------------------------------------------------------- sums
+    const int quarter = warp & 3, f = quarter * 32 + lane, rows = min(TN, p.M - m0);
+    const float bias = p.bias && f0 + f < p.N ? p.bias[f0 + f] : 0.f;
+    ok = tc::mbar_wait_warp(done, 0, abort_flag, p.status) && ok;
+    tc::tc_fence_after();
+    float* part = reinterpret_cast<float*>(codes_s);  // [TN][128], in the ring's place: every MMA has read it
+    if (ok)
+#pragma unroll
+      for (int c = 0; c < TN; c += 16) {
+        uint32_t v[16];
+        tc::tmem_ld16(tc::taddr(tmem, quarter * 32, c), v);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (C > 1) part[(c + i) * kTF + f] = __uint_as_float(v[i]);
+          else if (c + i < rows && f0 + f < p.N) p.Y[(size_t)(m0 + c + i) * p.N + f0 + f] = __float2bfloat16_rn(__uint_as_float(v[i]) + bias);
+        }
+      }
+    if (C > 1) {
+      __syncwarp();
+      cluster_sync();
+      // This block sums the tokens rank, rank + C, ...: four features a thread,
+      // the loads of four (token, features) from one peer in flight together.
+      const uint32_t at = tc::smem_u32(part);
+      const int mine = rows > rank ? (rows - rank + C - 1) / C : 0, col = lane * 4;
+      for (int j0 = quarter; ok && j0 < mine && f0 + col < p.N; j0 += 16) {
+        float4 s[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < C; ++i) {
+          const uint32_t peer = peer_address(at, i);
+          float4 v[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) v[u] = load_peer(peer + ((rank + min(j0 + 4 * u, mine - 1) * C) * kTF + col) * 4);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            s[u].x += v[u].x; s[u].y += v[u].y; s[u].z += v[u].z; s[u].w += v[u].w;
+          }
+        }
+        const float4 b = p.bias ? *reinterpret_cast<const float4*>(p.bias + f0 + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (j0 + 4 * u < mine) {
+            __nv_bfloat162 y[2] = {__floats2bfloat162_rn(s[u].x + b.x, s[u].y + b.y), __floats2bfloat162_rn(s[u].z + b.z, s[u].w + b.w)};
+            *reinterpret_cast<uint2*>(p.Y + (size_t)(m0 + rank + (j0 + 4 * u) * C) * p.N + f0 + col) = *reinterpret_cast<const uint2*>(y);
+          }
+      }
+      __syncwarp();
+    }
+  }
+  if (C > 1) {
+    if (warp < 4) {
+      __syncwarp();
+      cluster_sync();
+    }
+    cluster_sync();  // a block's partial sums stay until every block has read them
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::mbar_wait(done, 0, no_flag, p.status);
+    __syncwarp();
+    tc::tmem_dealloc(tmem, T::kAlloc);
+  }
+}
+
+template <int TN>
+cudaError_t launch_few(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_codes, cudaStream_t st) {
+  using T = FewTile<TN>;
+  CUtensorMap map_w, map_a;
+  if (!tma_map_u8_rows(&map_w, w_codes, p.K / 2, p.N, kTF) || !tma_map_u8_rows(&map_a, a_codes, p.K / 2, p.M, TN))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(k_mx_few<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+  if (e != cudaSuccess) return e;
+  p.ftiles = (p.N + kTF - 1) / kTF;
+  p.tiles = p.ftiles * ((p.M + TN - 1) / TN);
+  int C = 1;
+  while (C < 8 && p.tiles * C * 2 <= 160 && p.kblocks >= 4 * C) C *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.tiles * C);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = T::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = C;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, k_mx_few<TN>, map_w, map_a, p, C);
+  note_launch();
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
 template <int TN>
 cudaError_t launch(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_codes, cudaStream_t st) {
   using T = Tile<TN>;
@@ -353,8 +637,10 @@ cudaError_t mx_product_run(const uint8_t* a_codes, const uint8_t* a_scales, cons
   p.kblocks = (K + kKB - 1) / kKB;
   p.status = status_word();
   if (!p.status) return cudaErrorInvalidValue;
-  if (M <= 16) return launch<16>(p, a_codes, w_codes, st);
-  if (M <= 64) return launch<64>(p, a_codes, w_codes, st);
+  if (M <= 16) return launch_few<16>(p, a_codes, w_codes, st);
+  // From 65 tokens on the wide tiles win even where they leave SMs idle (256 tokens, N = K = 5,120: 15.0 us
+  // against 17.4 us in tiles of 64).
+  if (M <= 64) return launch_few<64>(p, a_codes, w_codes, st);
   return launch<192>(p, a_codes, w_codes, st);
 }
 

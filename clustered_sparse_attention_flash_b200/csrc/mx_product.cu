@@ -4,22 +4,15 @@
 //
 // tcgen05.mma kind::mxf4 multiplies E2M1 pairs exactly and applies one E8M0
 // scale per 32 elements of each operand; sums are float32 in tensor memory and
-// rounded once, to bf16.  The features are the MMA's 128 rows and the tokens
-// its columns, so that the tile narrows to 16 columns for a few tokens while
-// the weights still stream through full tiles.
+// rounded once, to bf16.  The features are the MMA's rows and the tokens its
+// columns, so that the tile narrows to 16 columns for a few tokens while the
+// weights still stream through full tiles.
 //
-// One persistent block per SM:
-//   warp 0       TMA: code tiles of 256 elements (128 bytes per row, 128-byte
-//                swizzle) into a ring of stages
-//   warp 1       tensor memory, copies of the scales into it, MMAs
-//   warps 4-7    scales: plain rows in global memory to the tensor core's
-//                order in shared memory (a 128-row, 4-scale atom is 512 bytes,
-//                row r at 16 (r mod 32) + 4 (r div 32))
-//   warps 8-11   epilogue: accumulators + bias to bf16 through shared memory
-//                into coalesced rows; two accumulators, so that it runs
-//                beside the next tile's MMAs
-// Scales keep one tensor-memory slot per ring stage: a slot is written again
-// only after the MMAs that read it have committed.
+// Scales lie as plain rows in global memory.  A warpgroup brings them into the
+// tensor core's order in shared memory (an atom of 128 rows x 4 scales is 512
+// bytes, row r at 16 (r mod 32) + 4 (r div 32)), from where tcgen05.cp takes
+// them to tensor memory.  They keep one tensor-memory slot per ring stage: a
+// slot is written again only after the MMAs that read it have committed.
 #include <cuda.h>
 
 #include <algorithm>
@@ -31,29 +24,10 @@ namespace svg {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kTF = 128;          // features per tile (MMA M)
+constexpr int kTF = 128;          // features per block
 constexpr int kKB = 256;          // elements of K per stage (128 bytes of codes)
 constexpr int kChunk = 32;        // tokens per epilogue step
 constexpr int kSmemLimit = 232448;
-
-// Tile of TN tokens (MMA N).
-template <int TN>
-struct Tile {
-  static constexpr int kTokBlocks = (TN + 127) / 128;        // 128-row scale atoms of the tokens
-  static constexpr int kCodesF = kTF * 128, kCodesT = TN * 128;
-  static constexpr int kSfF = 2 * 512, kSfT = 2 * 512 * kTokBlocks;
-  static constexpr int kStage = kCodesF + kCodesT + kSfF + kSfT;
-  static constexpr int kStages = TN > 128 ? 4 : TN > 64 ? 5 : 6;
-  static constexpr int kOut = 2 * kChunk * kTF * 2;          // two staging buffers, bf16
-  static constexpr int kBars = 256;
-  static constexpr int kSmem = kStages * kStage + kOut + kBars + 1024;
-  static constexpr int kAccCols = TN;                        // per accumulator, two of them
-  static constexpr int kSfCols = 8 + 8 * kTokBlocks;         // per stage: 2 atoms of features, 2 of each token block
-  static constexpr int kCols = 2 * kAccCols + kStages * kSfCols;
-  static constexpr int kAlloc = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-  static_assert(kCols <= 512 && kSmem <= kSmemLimit, "tile does not fit");
-};
 
 struct ProductArgs {
   const uint8_t *a_scales, *w_scales;
@@ -65,8 +39,8 @@ struct ProductArgs {
 
 // kind::mxf4, both operands E2M1, scales E8M0 (one per 32), M x N tile; ids
 // select the first or second scale pair of a 4-byte column.
-__host__ __device__ constexpr uint32_t idesc_mxf4(int N, uint32_t id) {
-  return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27) | (id << 4) | (id << 29);
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, uint32_t id) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 7) << 27) | (id << 4) | (id << 29);
 }
 
 __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
@@ -104,39 +78,165 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pitch, int 
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-template <int TN>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_mx_product(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, const ProductArgs p) {
-  using T = Tile<TN>;
-  constexpr int S = T::kStages;
+// ------------------------------------------------------------- many tokens
+//
+// Two neighbouring SMs work on one tile of 256 features x 192 tokens
+// (cta_group::2): each holds its own 128 features and half of the tokens, so
+// an SM reads 7 KB of codes per 64 elements of K where a tile of its own would
+// read 10 KB; the shared-memory port (written once by TMA, read once by the
+// MMA) is what bounds this kernel.  The even block issues the MMAs for both.
+//   warp 0       TMA: code tiles of 256 elements (128 bytes per row, 128-byte
+//                swizzle) into a ring of stages; both blocks' copies complete on
+//                the even block's barrier
+//   warp 1       tensor memory; in the even block scale copies and MMAs
+//   warps 4-7    scales of the block's features and of all the tile's tokens, in
+//                units of two stages and a ring of their own, eight units deep
+//   warps 1-3    in the odd block: pass the word that an accumulator has been
+//                read (1) or a unit is there (2, 3) on to the even block.  The release over the cluster that this takes
+//                costs about a thousand cycles (and would wait for the scale
+//                warps' loads in flight): hence warps of their own and the deep
+//                ring.  (75,600 x 15,360 x 5,120: 6.61 ms with the scale warps
+//                releasing, 4.15 ms with a ring of five stages, then see below.)
+//   warps 8-11   epilogue: accumulators + bias to bf16 through shared memory
+//                into coalesced rows; two accumulators, so that it runs beside
+//                the next tile's MMAs
+
+constexpr int kPairThreads = 384;
+constexpr int kPairTokens = 192;
+
+struct Pair {
+  static constexpr int kTokBlocks = 2;                             // 128-row scale atoms of the tokens
+  static constexpr int kCodesF = kTF * 128, kCodesT = kPairTokens / 2 * 128, kCodes = kCodesF + kCodesT;
+  static constexpr int kSfF = 2 * 512, kSf = kSfF + 2 * 512 * kTokBlocks;  // scales of a stage
+  static constexpr int kStages = 5, kUnits = 8;
+  static constexpr int kOut = 2 * kChunk * kTF * 2;                // two staging buffers, bf16
+  static constexpr int kBars = 512;
+  static constexpr int kSmem = kStages * kCodes + kUnits * 2 * kSf + kOut + kBars + 1024;
+  static constexpr int kSfCols = 8 + 8 * kTokBlocks;               // per stage: 2 atoms of features, 2 of each token block
+  static_assert(2 * kPairTokens + kStages * kSfCols <= 512 && kSmem <= kSmemLimit && kCodes % 1024 == 0, "tile does not fit");
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of every block of the cluster (warps converged).
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_address(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 load_peer(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// The address of a barrier of the even block.
+__device__ __forceinline__ uint32_t leader_address(const uint64_t* bar) { return peer_address(tc::smem_u32(bar), 0); }
+__device__ __forceinline__ void arrive_leader(const uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_address(bar)) : "memory");
+}
+// tc::mbar_wait_warp for barriers that the other block arrives at.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  bool ok = false;
+  const uint64_t t0 = tc::globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) {
+      ok = true;
+      break;
+    }
+    if ((it & 255u) == 0) {
+      if (*abort_flag) break;
+      if (tc::globaltimer() - t0 > tc::kWaitLimitNs) {
+        set_status(status, ST_TIMEOUT);
+        *abort_flag = 1;
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(0), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void copy_scales_pair(uint32_t taddr, uint32_t saddr) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(tc::sdesc(saddr, 128, 128, 0)) : "memory");
+}
+__device__ __forceinline__ void mma_mxf4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+// Arrive on `bar` of both blocks once every MMA and copy issued so far is done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          tc::smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    k_mx_pair(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, const ProductArgs p) {
+  using T = Pair;
+  constexpr int S = T::kStages, U = T::kUnits, TN = kPairTokens;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // code tiles first (1,024-byte aligned), then the scales of all stages, then the output staging
+  // the dynamic part starts at the same offset in both blocks, and so does all of this
+  uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* codes_s = smem;
-  uint8_t* sf_s = smem + S * (T::kCodesF + T::kCodesT);
-  bf16* out_s = reinterpret_cast<bf16*>(sf_s + S * (T::kSfF + T::kSfT));
+  uint8_t* sf_s = smem + S * T::kCodes;
+  bf16* out_s = reinterpret_cast<bf16*>(sf_s + U * 2 * T::kSf);
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(out_s) + T::kOut);
-  uint64_t* codes_full = bars;            // [S]
-  uint64_t* sf_full = bars + S;           // [S]
-  uint64_t* empty = bars + 2 * S;         // [S]
-  uint64_t* acc_full = bars + 3 * S;      // [2]
-  uint64_t* acc_empty = bars + 3 * S + 2; // [2]
-  uint64_t* done = bars + 3 * S + 4;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 5);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 3 * S + 6);
+  uint64_t* codes_full = bars;            // [S] of the even block: both blocks' codes
+  uint64_t* empty = codes_full + S;       // [S]
+  uint64_t* sf_full = empty + S;          // [U] own scales; in the even block the other's word too
+  uint64_t* sf_empty = sf_full + U;       // [U]
+  uint64_t* acc_full = sf_empty + U;      // [2]
+  uint64_t* acc_empty = acc_full + 2;     // [2] own epilogue; in the even block the other's word too
+  uint64_t* done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(done + 2);
   volatile int* no_flag = abort_flag + 1;  // stays 0: waits that an abort must not cut short
-  static_assert((3 * S + 7) * 8 <= T::kBars, "barrier area");
+  static_assert((2 * S + 2 * U + 7) * 8 <= T::kBars, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       tc::mbar_init(codes_full + i, 1);
-      tc::mbar_init(sf_full + i, 4);
       tc::mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < U; ++i) {
+      tc::mbar_init(sf_full + i, rank == 0 ? 5 : 4);
+      tc::mbar_init(sf_empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(acc_full + i, 1);
-      tc::mbar_init(acc_empty + i, 4);
+      tc::mbar_init(acc_empty + i, rank == 0 ? 5 : 4);
     }
     tc::mbar_init(done, 1);
     *abort_flag = 0;
@@ -144,11 +244,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_fence_init();
   }
   if (warp == 1) {
-    tc::tmem_alloc(tmem_slot, T::kAlloc);
-    tc::tmem_relinquish();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc::tc_fence_before();
   __syncthreads();
+  cluster_sync();  // both blocks' barriers are there, and their tensor memory
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -159,73 +260,97 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tma_prefetch_map(&map_a);
       uint32_t it = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
-        const int f0 = t % p.ftiles * kTF, m0 = t / p.ftiles * TN;
+      for (int t = first; ok && t < p.tiles; t += stride) {
+        const int f0 = (t % p.ftiles * 2 + rank) * kTF, m0 = t / p.ftiles * TN + rank * (TN / 2);
         for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
           const int s = it % S;
           ok = tc::mbar_wait(empty + s, (it / S & 1) ^ 1, abort_flag, p.status);
           if (!ok) break;
-          const uint32_t dst = tc::smem_u32(codes_s + s * (T::kCodesF + T::kCodesT));
-          tc::mbar_arrive_expect_tx(codes_full + s, T::kCodesF + T::kCodesT);
-          tc::tma_load_3d(dst, &map_w, kb * (kKB / 2), f0, 0, codes_full + s);
-          tc::tma_load_3d(dst + T::kCodesF, &map_a, kb * (kKB / 2), m0, 0, codes_full + s);
+          const uint32_t dst = tc::smem_u32(codes_s + s * T::kCodes), bar = leader_address(codes_full + s);
+          if (rank == 0) tc::mbar_arrive_expect_tx(codes_full + s, 2 * T::kCodes);
+          tma_load_pair(dst, &map_w, kb * (kKB / 2), f0, bar);
+          tma_load_pair(dst + T::kCodesF, &map_a, kb * (kKB / 2), m0, bar);
         }
       }
-      // The block's memory outlives its copies, also after an abort.
-      for (uint32_t i = it > S ? it - S : 0; i < it; ++i) tc::mbar_wait(codes_full + i % S, i / S & 1, no_flag, p.status);
+      // The blocks' memory outlives their copies, also after an abort (both blocks meet below).
+      if (rank == 0)
+        for (uint32_t i = it > S ? it - S : 0; i < it; ++i) tc::mbar_wait(codes_full + i % S, i / S & 1, no_flag, p.status);
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 1 && rank == 0) {
     // -------------------------------------------------------------- MMAs
     const bool leader = tc::elect_one();
-    uint32_t it = 0, n = 0;
+    uint32_t it = 0, un = 0, n = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, ++n) {
-      const uint32_t buf = n & 1, acc = tmem + buf * T::kAccCols;
-      ok = tc::mbar_wait_warp(acc_empty + buf, (n >> 1 & 1) ^ 1, abort_flag, p.status);
+    for (int t = first; ok && t < p.tiles; t += stride, ++n) {
+      const uint32_t buf = n & 1, acc = tmem + buf * TN;
+      ok = wait_cluster(acc_empty + buf, (n >> 1 & 1) ^ 1, abort_flag, p.status);
       for (int kb = 0; ok && kb < p.kblocks; ++kb, ++it) {
-        const int s = it % S;
-        ok = tc::mbar_wait_warp(codes_full + s, it / S & 1, abort_flag, p.status) &&
-             tc::mbar_wait_warp(sf_full + s, it / S & 1, abort_flag, p.status);
+        const int s = it % S, u = un % U, h = kb & 1;  // a unit's two stages
+        if (h == 0) ok = wait_cluster(sf_full + u, un / U & 1, abort_flag, p.status);
+        ok = ok && tc::mbar_wait_warp(codes_full + s, it / S & 1, abort_flag, p.status);
         if (!ok) break;
         tc::tc_fence_after();
-        const uint32_t wf = tc::smem_u32(codes_s + s * (T::kCodesF + T::kCodesT)), tk = wf + T::kCodesF;
-        const uint32_t sf = tc::smem_u32(sf_s + s * (T::kSfF + T::kSfT));
-        const uint32_t tf = tmem + 2 * T::kAccCols + s * T::kSfCols, tt = tf + 8;
+        const uint32_t wf = tc::smem_u32(codes_s + s * T::kCodes), tk = wf + T::kCodesF;
+        const uint32_t sf = tc::smem_u32(sf_s + (u * 2 + h) * T::kSf);
+        const uint32_t tf = tmem + 2 * TN + s * T::kSfCols, tt = tf + 8;
+        const bool last = kb + 1 == p.kblocks;
         if (leader) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            copy_scales(tf + i * 4, sf + i * 512);
+            copy_scales_pair(tf + i * 4, sf + i * 512);
 #pragma unroll
             for (int b = 0; b < T::kTokBlocks; ++b)
-              copy_scales(tt + (i * T::kTokBlocks + b) * 4, sf + T::kSfF + (i * T::kTokBlocks + b) * 512);
+              copy_scales_pair(tt + (i * T::kTokBlocks + b) * 4, sf + T::kSfF + (i * T::kTokBlocks + b) * 512);
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_mxf4(acc, tc::desc_kmajor(wf, 0, k), tc::desc_kmajor(tk, 0, k), idesc_mxf4(TN, (k & 1) * 2), tf + (k >> 1) * 4,
-                     tt + (k >> 1) * T::kTokBlocks * 4, (kb | k) ? 1u : 0u);
-          tc::mma_commit(empty + s);
-          if (kb + 1 == p.kblocks) tc::mma_commit(acc_full + buf);
+            mma_mxf4_pair(acc, tc::desc_kmajor(wf, 0, k), tc::desc_kmajor(tk, 0, k), idesc_mxf4(2 * kTF, TN, (k & 1) * 2),
+                          tf + (k >> 1) * 4, tt + (k >> 1) * T::kTokBlocks * 4, (kb | k) ? 1u : 0u);
+          commit_pair(empty + s);
+          if (h == 1 || last) commit_pair(sf_empty + u);
+          if (last) commit_pair(acc_full + buf);
         }
+        if (h == 1 || last) ++un;
         __syncwarp();
       }
     }
-    if (leader) tc::mma_commit(done);
+    if (leader) commit_pair(done);
     __syncwarp();
+  } else if (warp == 1) {
+    // Odd block: the word that an accumulator has been read.
+    uint32_t n = 0;
+    bool ok = true;
+    for (int t = first; ok && t < p.tiles; t += stride, ++n) {
+      ok = tc::mbar_wait_warp(acc_empty + (n & 1), n >> 1 & 1, abort_flag, p.status);
+      if (ok && lane == 0) arrive_leader(acc_empty + (n & 1));
+      __syncwarp();
+    }
+  } else if ((warp == 2 || warp == 3) && rank == 1) {
+    // Every other unit each.
+    const int units = (p.kblocks + 1) / 2;
+    uint32_t un = 0;
+    bool ok = true;
+    for (int t = first; ok && t < p.tiles; t += stride)
+      for (int i = 0; ok && i < units; ++i, ++un) {
+        if ((un & 1) != (warp & 1)) continue;
+        ok = tc::mbar_wait_warp(sf_full + un % U, un / U & 1, abort_flag, p.status);
+        if (ok && lane == 0) arrive_leader(sf_full + un % U);
+        __syncwarp();
+      }
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ scales
-    // Row r of the features and rows r, r + 128 of the tokens.  A load takes the
-    // scales of two stages and runs two loads (two to four stages) ahead of
-    // the stores, over tile boundaries too.
+    // Row r of the block's features and rows r, r + 128 of the tokens, loaded two
+    // units ahead of the stores, over tile boundaries too.
     const int r = threadIdx.x - 128;
     const int pitch = p.K / 32, units = (p.kblocks + 1) / 2;
     constexpr int R = T::kTokBlocks;
     struct Unit {
       uint4 v[R + 1];
     };
-    int ft = blockIdx.x, fu = 0;  // the next unit to load
+    int ft = first, fu = 0;  // the next unit to load
     auto fetch = [&](Unit& x) {
-      const int f = ft % p.ftiles * kTF + r, m0 = ft / p.ftiles * TN;
+      const int f = (ft % p.ftiles * 2 + rank) * kTF + r, m0 = ft / p.ftiles * TN;
       const bool more = ft < p.tiles;
       x.v[0] = more && f < p.N ? load_scales(p.w_scales + (size_t)f * pitch, pitch, fu) : make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -235,71 +360,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (++fu == units) {
         fu = 0;
-        ft += gridDim.x;
+        ft += stride;
       }
-    };
-    uint32_t it = 0;
-    bool ok = true;
-    auto store = [&](const Unit& x, int h) {
-      const int s = it % S;
-      ok = tc::mbar_wait_warp(empty + s, (it / S & 1) ^ 1, abort_flag, p.status);
-      if (!ok) return;
-      uint8_t* sf = sf_s + s * (T::kSfF + T::kSfT) + (r & 31) * 16 + (r >> 5) * 4;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        *reinterpret_cast<uint32_t*>(sf + i * 512) = h ? (i ? x.v[0].w : x.v[0].z) : (i ? x.v[0].y : x.v[0].x);
-#pragma unroll
-        for (int b = 0; b < R; ++b)
-          *reinterpret_cast<uint32_t*>(sf + T::kSfF + (i * R + b) * 512) =
-              h ? (i ? x.v[b + 1].w : x.v[b + 1].z) : (i ? x.v[b + 1].y : x.v[b + 1].x);
-      }
-      tc::fence_proxy_async();  // the tensor core's copies read what this thread stored
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(sf_full + s);
-      ++it;
     };
     Unit x0, x1, x2;
     fetch(x0);
     fetch(x1);
-    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x)
-      for (int u = 0; ok && u < units; ++u) {
+    uint32_t un = 0;
+    bool ok = true;
+    for (int t = first; ok && t < p.tiles; t += stride)
+      for (int i = 0; i < units; ++i, ++un) {
         fetch(x2);
-        store(x0, 0);
-        if (ok && 2 * u + 1 < p.kblocks) store(x0, 1);
+        ok = tc::mbar_wait_warp(sf_empty + un % U, (un / U & 1) ^ 1, abort_flag, p.status);
+        if (!ok) break;
+        // the four words of a row: stage 0 atoms 0, 1, stage 1 atoms 0, 1
+        uint8_t* sf = sf_s + un % U * 2 * T::kSf + (r & 31) * 16 + (r >> 5) * 4;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint8_t* at = sf + (q >> 1) * T::kSf;
+          auto word = [&](const uint4& v) { return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w; };
+          *reinterpret_cast<uint32_t*>(at + (q & 1) * 512) = word(x0.v[0]);
+#pragma unroll
+          for (int b = 0; b < R; ++b) *reinterpret_cast<uint32_t*>(at + T::kSfF + ((q & 1) * R + b) * 512) = word(x0.v[b + 1]);
+        }
+        tc::fence_proxy_async();  // the tensor core's copies read what this thread stored
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(sf_full + un % U);
         x0 = x1;
         x1 = x2;
       }
   } else if (warp >= 8) {
     // ---------------------------------------------------------- epilogue
     const int quarter = warp & 3, f = quarter * 32 + lane, tid = threadIdx.x - 256;
-    constexpr int C = TN < kChunk ? TN : kChunk;
     uint32_t n = 0, step = 0;
-    for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, ++n) {
-      const int f0 = t % p.ftiles * kTF, m0 = t / p.ftiles * TN;
+    for (int t = first; t < p.tiles; t += stride, ++n) {
+      const int f0 = (t % p.ftiles * 2 + rank) * kTF, m0 = t / p.ftiles * TN;
       const uint32_t buf = n & 1;
       const float bias = p.bias && f0 + f < p.N ? p.bias[f0 + f] : 0.f;
       if (!tc::bar_and(1, 128, tc::mbar_wait_warp(acc_full + buf, n >> 1 & 1, abort_flag, p.status))) break;
       tc::tc_fence_after();
       const int rows = min(TN, p.M - m0);
-      for (int c = 0; c < TN; c += C, ++step) {
-        if (c >= rows) break;  // uniform: tokens behind the last one
+      for (int c = 0; c < rows; c += kChunk, ++step) {
         uint32_t v[32];
-        const uint32_t at = tc::taddr(tmem, quarter * 32, buf * T::kAccCols + c);
-        if constexpr (C == 32) {
-          tc::tmem_ld32(at, v);
-        } else {
-          uint32_t w[16];
-          tc::tmem_ld16(at, w);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = w[i];
-        }
+        tc::tmem_ld32(tc::taddr(tmem, quarter * 32, buf * TN + c), v);
         tc::tmem_ld_wait();
         bf16* st = out_s + (step & 1) * (kChunk * kTF);
 #pragma unroll
-        for (int i = 0; i < C; ++i) st[i * kTF + f] = __float2bfloat16_rn(__uint_as_float(v[i]) + bias);
+        for (int i = 0; i < kChunk; ++i) st[i * kTF + f] = __float2bfloat16_rn(__uint_as_float(v[i]) + bias);
         asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
-        for (int u = 0; u < C / 8; ++u) {
+        for (int u = 0; u < kChunk / 8; ++u) {
           const int e = u * 128 + tid, m = e >> 4, col = (e & 15) * 8;
           if (c + m < rows && f0 + col < p.N)
             *reinterpret_cast<uint4*>(p.Y + (size_t)(m0 + c + m) * p.N + f0 + col) = *reinterpret_cast<const uint4*>(st + m * kTF + col);
@@ -317,8 +427,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tc_fence_after();
     tc::mbar_wait(done, 0, no_flag, p.status);
     __syncwarp();
-    tc::tmem_dealloc(tmem, T::kAlloc);
   }
+  __syncthreads();
+  cluster_sync();  // neither block's memory is in use by the other any more
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 // ------------------------------------------------------------- few tokens
@@ -344,29 +456,6 @@ struct FewTile {
   static constexpr int kAlloc = TN + kStages * kSfCols <= 128 ? 128 : 256;
   static_assert(kStages * kCodes >= TN * kTF * 4, "partial sums take the ring's place");
 };
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// Every thread of every block of the cluster (warps converged).
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t peer_address(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 load_peer(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
 
 // Scales [8 kb, 8 kb + 8) of a row with `pitch` scales (one stage); 0 behind the end.
 __device__ __forceinline__ uint2 load_scales8(const uint8_t* row, int pitch, int kb) {
@@ -462,7 +551,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         for (int i = 0; i < 4; ++i) copy_scales(tf + i * 4, sf + i * 512);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_mxf4(tmem, tc::desc_kmajor(wf, 0, k), tc::desc_kmajor(tk, 0, k), idesc_mxf4(TN, (k & 1) * 2), tf + (k >> 1) * 4,
+          mma_mxf4(tmem, tc::desc_kmajor(wf, 0, k), tc::desc_kmajor(tk, 0, k), idesc_mxf4(kTF, TN, (k & 1) * 2), tf + (k >> 1) * 4,
                    tf + 8 + (k >> 1) * 4, (it | k) ? 1u : 0u);
         tc::mma_commit(empty + s);
       }
@@ -605,17 +694,15 @@ cudaError_t launch_few(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_c
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <int TN>
-cudaError_t launch(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_codes, cudaStream_t st) {
-  using T = Tile<TN>;
+cudaError_t launch_pair(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_codes, cudaStream_t st) {
   CUtensorMap map_w, map_a;
-  if (!tma_map_u8_rows(&map_w, w_codes, p.K / 2, p.N, kTF) || !tma_map_u8_rows(&map_a, a_codes, p.K / 2, p.M, TN))
+  if (!tma_map_u8_rows(&map_w, w_codes, p.K / 2, p.N, kTF) || !tma_map_u8_rows(&map_a, a_codes, p.K / 2, p.M, kPairTokens / 2))
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(k_mx_product<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(k_mx_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, Pair::kSmem);
   if (e != cudaSuccess) return e;
-  p.ftiles = (p.N + kTF - 1) / kTF;
-  p.tiles = p.ftiles * ((p.M + TN - 1) / TN);
-  k_mx_product<TN><<<std::min(p.tiles, 148), kThreads, T::kSmem, st>>>(map_w, map_a, p);
+  p.ftiles = (p.N + 2 * kTF - 1) / (2 * kTF);
+  p.tiles = p.ftiles * ((p.M + kPairTokens - 1) / kPairTokens);
+  k_mx_pair<<<2 * std::min(p.tiles, 74), kPairThreads, Pair::kSmem, st>>>(map_w, map_a, p);
   note_launch();
   return cudaGetLastError();
 }
@@ -638,10 +725,9 @@ cudaError_t mx_product_run(const uint8_t* a_codes, const uint8_t* a_scales, cons
   p.status = status_word();
   if (!p.status) return cudaErrorInvalidValue;
   if (M <= 16) return launch_few<16>(p, a_codes, w_codes, st);
-  // From 65 tokens on the wide tiles win even where they leave SMs idle (256 tokens, N = K = 5,120: 15.0 us
-  // against 17.4 us in tiles of 64).
+  // From 65 tokens on the wide tiles win even where they leave SMs idle.
   if (M <= 64) return launch_few<64>(p, a_codes, w_codes, st);
-  return launch<192>(p, a_codes, w_codes, st);
+  return launch_pair(p, a_codes, w_codes, st);
 }
 
 }  // namespace svg

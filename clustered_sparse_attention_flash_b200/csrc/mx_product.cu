@@ -52,6 +52,10 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
       : "memory");
 }
 
+// The row whose scales thread t of the scale warps stores: word t of an atom, so
+// that a warp's stores meet no bank twice (row t itself would four times).
+__device__ __forceinline__ int scale_row(int t) { return (t & 3) * 32 + (t >> 2); }
+
 // One scale atom (32 rows of 16 bytes in shared memory) into 4 tensor-memory
 // columns, for all four lane quarters.
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
@@ -342,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ------------------------------------------------------------ scales
     // Row r of the block's features and rows r, r + 128 of the tokens, loaded two
     // units ahead of the stores, over tile boundaries too.
-    const int r = threadIdx.x - 128;
+    const int r = scale_row(threadIdx.x - 128);
     const int pitch = p.K / 32, units = (p.kblocks + 1) / 2;
     constexpr int R = T::kTokBlocks;
     struct Unit {
@@ -374,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         ok = tc::mbar_wait_warp(sf_empty + un % U, (un / U & 1) ^ 1, abort_flag, p.status);
         if (!ok) break;
         // the four words of a row: stage 0 atoms 0, 1, stage 1 atoms 0, 1
-        uint8_t* sf = sf_s + un % U * 2 * T::kSf + (r & 31) * 16 + (r >> 5) * 4;
+        uint8_t* sf = sf_s + un % U * 2 * T::kSf + (threadIdx.x - 128) * 4;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint8_t* at = sf + (q >> 1) * T::kSf;
@@ -562,7 +566,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   } else if (warp >= 4) {
     // ------------------------------------------------------------ scales
     // Row r of the features and of the tokens, four stages loaded ahead.
-    const int r = threadIdx.x - 128, pitch = p.K / 32;
+    const int r = scale_row(threadIdx.x - 128), pitch = p.K / 32;
     const uint8_t* wrow = f0 + r < p.N ? p.w_scales + (size_t)(f0 + r) * pitch : nullptr;
     const uint8_t* arow = r < TN && m0 + r < p.M ? p.a_scales + (size_t)(m0 + r) * pitch : nullptr;
     constexpr int B = 4;
@@ -584,7 +588,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         const int it = kb + i - kb0, s = it % S;
         ok = tc::mbar_wait_warp(empty + s, (it / S & 1) ^ 1, abort_flag, p.status);
         if (!ok) break;
-        uint8_t* sf = sf_s + s * T::kSf + (r & 31) * 16 + (r >> 5) * 4;
+        uint8_t* sf = sf_s + s * T::kSf + (threadIdx.x - 128) * 4;
         *reinterpret_cast<uint32_t*>(sf) = cw[i].x;
         *reinterpret_cast<uint32_t*>(sf + 512) = cw[i].y;
         *reinterpret_cast<uint32_t*>(sf + 1024) = ca[i].x;

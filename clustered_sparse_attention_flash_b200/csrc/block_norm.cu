@@ -218,6 +218,7 @@ struct Direct {
     }
   }
   __device__ __forceinline__ void release(int) {}
+  __device__ __forceinline__ void release_previous(int) {}
 };
 
 constexpr int kMaxStages = 16;
@@ -225,7 +226,7 @@ constexpr int kMaxStages = 16;
 template <typename TX, typename TY, int OPS, int V>
 struct Ring {
   const NormArgs& p;
-  int end;
+  int first, end;
   uint32_t bx, by, stage;  // bytes of a row of either type, of a stage
   uint32_t col[V];
   uint8_t* buf;
@@ -245,8 +246,8 @@ struct Ring {
       if (p.dh) tc::bulk_g2s(dst + 2 * bx + by, static_cast<const char*>(p.dh) + (long long)row * by, by, full + s);
     }
   }
-  __device__ __forceinline__ Ring(const NormArgs& args, const Columns<V>& cols, int first, int last)
-      : p(args), end(last), slot(-1), parity(1) {
+  __device__ __forceinline__ Ring(const NormArgs& args, const Columns<V>& cols, int row, int last)
+      : p(args), first(row), end(last), slot(-1), parity(1) {
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ uint64_t bars[kMaxStages];
     __shared__ int flag;
@@ -287,6 +288,10 @@ struct Ring {
   // Behind a barrier that every thread reached after its last read of `row`.
   __device__ __forceinline__ void release(int row) {
     if (threadIdx.x == 0) issue(row + p.stages, slot);
+  }
+  // Behind a barrier in `row`: the row before it has been read by every thread.
+  __device__ __forceinline__ void release_previous(int row) {
+    if (threadIdx.x == 0 && row != first) issue(row - 1 + p.stages, slot == 0 ? p.stages - 1 : slot - 1);
   }
 };
 
@@ -458,6 +463,53 @@ __global__ void __launch_bounds__(Class<CLS, false>::kMax, (Class<CLS, false>::k
   }
 }
 
+// What the gradient of a norm's input needs of its row r and of u, the gradient
+// of the normalised row n: R = inv (u - mu - n mun), mu = mean(u) (layer norm
+// only), mun = mean(u n).  One barrier for all of it: with the squares go
+// sum u and sum u (r - mean_w) of every warp, joined by
+//   sum u (r - mean) = sum_w c_w + (mean_w - mean) sum_w u.
+struct BackStats {
+  float mean, inv, mu, mun;
+};
+template <int V, typename SUM>
+__device__ __forceinline__ BackStats back_statistics(const Vec (&r)[V], const Vec (&u)[V], const Columns<V>& c, int kind,
+                                                     float eps, SUM& sum) {
+  if (kind == SVGEAR_NORM_NONE) return {0.f, 1.f, 0.f, 0.f};
+  auto dot = [&](float mean) {
+    float s = 0.f;
+    const f2 m = pair(-mean);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      f2 q = pair(0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q = fma2(u[v].v[i], add2(r[v].v[i], m), q);
+      const float2 h = halves(q);
+      s += c.on[v] ? h.x + h.y : 0.f;
+    }
+    return s;
+  };
+  if (kind == SVGEAR_NORM_RMS) {
+    const float2 q = sum(make_float2(squares(r, c, 0.f), dot(0.f)));
+    const float inv = rsqrtf(fmaf(q.x, c.inv_d, eps));
+    return {0.f, inv, 0.f, q.y * c.inv_d * inv};
+  }
+  const float s = sum.lanes(total(r, c));
+  const float pivot = SUM::kBlock ? s * c.inv_own : over(s, c.d, c.inv_d);
+  float q = sum.lanes(squares(r, c, pivot));
+  float2 w = sum.lanes(make_float2(total(u, c), dot(pivot)));
+  float mean = pivot;
+  if (SUM::kBlock) {
+    float2 v = make_float2(s, q);
+    sum.trade(v, w);
+    mean = over(sum.warps(v.x), c.d, c.inv_d);
+    const float e = v.x * c.inv_n - mean;
+    q = sum.warps(fmaf(c.n * e, e, v.y));
+    w = make_float2(sum.warps(w.x), sum.warps(fmaf(e, w.x, w.y)));
+  }
+  const float inv = rsqrtf(fmaf(q, c.inv_d, eps));
+  return {mean, inv, w.x * c.inv_d, w.y * c.inv_d * inv};
+}
+
 // du -> the gradient of the norm's input: inv (du - n mean(du n) - mean(du)),
 // the last term for a layer norm only.  n is the normalised row.
 template <int V, typename SUM>
@@ -489,7 +541,7 @@ template <typename TX, typename TY, int CLS>
 __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kThreads / Class<CLS, true>::kMax))
     k_block_norm_back(const __grid_constant__ NormArgs p) {
   constexpr int V = Class<CLS, true>::kV;
-  __shared__ float2 scratch[64];
+  __shared__ float2 scratch[128];
   Sum<CLS> sum(scratch, p.tpr);
   const Place pl = place(p);
   Columns<V> c;
@@ -497,6 +549,9 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
   typename std::conditional<CLS == 0, Direct<TX, TY, 4, V>, Ring<TX, TY, 4, V>>::type rows(p, c, pl.row, pl.end);
   int g = pl.row < pl.end ? group_of(p, pl.row) : 0;
   int gend = pl.row;
+  // Rows are read to the end of their iteration.  With four stages or more the
+  // barrier in the next row's sum frees them; otherwise one at the end does.
+  const bool late = p.dh && p.pre != SVGEAR_NORM_NONE && p.stages > 3;
   const f2 a = pair(p.y ? p.a : 1.f);
   Coefficients<V, CLS != 0> k(p, c, coefficient_memory(p));
   Vec s1[V], s2[V], su[V];
@@ -544,21 +599,29 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
       }
     }
     if (p.dh) {
-      const float inv_n = normalise<V>(n, c, p.pre, p.eps, sum);
       rows.template read<kDh>(R);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const Vec ca = k.get_a(v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (CLS != 0 || live) {
-            s1[v].v[i] = add2(s1[v].v[i], R[v].v[i]);
-            s2[v].v[i] = fma2(R[v].v[i], n[v].v[i], s2[v].v[i]);
-          }
+          if (CLS != 0 || live) s1[v].v[i] = add2(s1[v].v[i], R[v].v[i]);
           R[v].v[i] = mul2(R[v].v[i], ca.v[i]);
         }
       }
-      norm_back<V>(R, n, c, inv_n, p.pre, sum);
+      const BackStats st = back_statistics<V>(n, R, c, p.pre, p.eps, sum);
+      if (late) rows.release_previous(row);
+      const f2 mean = pair(-st.mean), inv = pair(st.inv), mu = pair(-st.mu), mun = pair(-st.mun);
+      Vec dh[V];
+      rows.template read<kDh>(dh);  // again: kept in registers it would cost the fourth block per SM
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f2 x = mul2(add2(n[v].v[i], mean), inv);
+          if (CLS != 0 || live) s2[v].v[i] = fma2(dh[v].v[i], x, s2[v].v[i]);
+          R[v].v[i] = mul2(inv, add2(fma2(x, mun, mu), R[v].v[i]));
+        }
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) fill(R[v], 0.f);
@@ -577,7 +640,7 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
       if (live && c.on[v]) store_vec(static_cast<TX*>(p.dx) + out + c.col[v], n[v]);
     }
     if (p.y) {
-      rows.template read<kY>(n);  // again: kept in registers it would cost the fourth block per SM
+      rows.template read<kY>(n);  // again, like dh
       if (p.post != SVGEAR_NORM_NONE) apply<V>(n, st_m);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -593,8 +656,10 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
       for (int v = 0; v < V; ++v)
         if (live && c.on[v]) store_vec(static_cast<TY*>(p.dy) + out + c.col[v], R[v]);
     }
-    if (CLS != 0) __syncthreads();  // the row has been read
-    rows.release(row);
+    if (CLS != 0 && !late) {
+      __syncthreads();  // the row has been read
+      rows.release(row);
+    }
   }
   if (pl.row < pl.end) flush();
 }

@@ -137,7 +137,7 @@ __device__ __forceinline__ void fill(Vec& f, float x) {
 // Sums over the lanes of a worker.  STEPS < 0: `width` = 4, 8, 16 or 32 lanes of
 // a warp.  Otherwise a whole block of `width` / 32 <= 2^STEPS warps; every
 // thread of the block calls it the same number of times.  `scratch` ([2][32], for
-// `both` [4][32]) alternates between two halves, so one barrier per sum
+// two pairs at once [4][32]) alternates between two halves, so one barrier per sum
 // suffices: a half is written again only behind the next sum's barrier, which
 // every reader of it has reached.
 template <int STEPS>
@@ -182,15 +182,19 @@ struct RowSum {
     }
     return v;
   }
-  // Two pairs behind one barrier.
+  // Trades two pairs behind one barrier.
+  __device__ __forceinline__ void trade(float2& a, float2& b) {
+    float2* s = scratch + 64 + phase * 32;
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = b;
+    a = trade(a);
+    b = other(s);
+  }
+  // Sums of two pairs behind one barrier.
   __device__ __forceinline__ void both(float2& a, float2& b) {
     a = lanes(a);
     b = lanes(b);
     if (kBlock) {
-      float2* s = scratch + 64 + phase * 32;
-      if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = b;
-      a = trade(a);
-      b = other(s);
+      trade(a, b);
       a = make_float2(warps(a.x), warps(a.y));
       b = make_float2(warps(b.x), warps(b.y));
     }

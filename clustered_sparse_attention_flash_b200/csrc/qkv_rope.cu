@@ -38,7 +38,7 @@ struct RopeArgs {
   const int32_t* pos;
   long long pos_batch;  // int32 per batch entry (0: shared)
   float* part;          // backward: [workers][2][C] partial weight gradients
-  int B, N, H, d, out_tokens, norm, tpt, chunk, stages, ring_bytes, weight_bytes, table_tokens, grads_at;
+  int B, N, H, out_tokens, norm, tpt, chunk, stages, ring_bytes, weight_bytes, table_tokens, grads_at;
   int pairs0, pairs01, pairs;  // pairs of axis 0, of axes 0-1, of all axes
   int g1, g2, vol;             // grid extents of axes 1 and 2, grid tokens
   int origin[3];
@@ -156,20 +156,22 @@ __device__ __forceinline__ float dot(const Sixteen& x, const Sixteen& y) {
 }
 
 // Where a thread works: its worker, its place in a token, its run of tokens.
+template <int D>
 struct Place {
-  int slot, lane, lanes, j, head, off;  // off: element offset of the low vector in a token
+  static constexpr int lanes = D / 16;
+  int slot, lane, j, head, off;  // off: element offset of the low vector in a token
   bool on;
   int t, end;                           // tokens [t, end), counted b * N + n
 };
-__device__ __forceinline__ Place place(const RopeArgs& p) {
-  Place q;
+template <int D>
+__device__ __forceinline__ Place<D> place(const RopeArgs& p) {
+  Place<D> q;
   q.slot = threadIdx.x / p.tpt;
   q.lane = threadIdx.x - q.slot * p.tpt;
-  q.lanes = p.d / 16;
   q.head = q.lane / q.lanes;
   q.j = q.lane - q.head * q.lanes;
   q.on = q.head < p.H;
-  q.off = q.head * p.d + q.j * kVec;
+  q.off = q.head * D + q.j * kVec;
   const long long total = (long long)p.B * p.N, first = ((long long)blockIdx.x * (blockDim.x / p.tpt) + q.slot) * p.chunk;
   q.t = (int)min(first, total);
   q.end = (int)min(first + p.chunk, total);
@@ -194,10 +196,10 @@ __device__ __forceinline__ uint8_t* shared_base() {
 
 // SHARED: in shared memory, each thread its own elements; otherwise (tokens too
 // wide for that) read from global memory, where they stay in the L1.
-template <bool HALF, bool SHARED>
+template <bool HALF, bool SHARED, int D>
 struct Weights {
   const RopeArgs& p;
-  const Place& pl;
+  const Place<D>& pl;
   ulonglong2* at;
   __device__ __forceinline__ void load(int k, Sixteen& z) const {
     const int o = p.norm == SVGEAR_QKNORM_TOKEN ? pl.off : pl.j * kVec;
@@ -205,12 +207,12 @@ struct Weights {
     lo.a = lo.b = hi.a = hi.b = make_float4(1.f, 1.f, 1.f, 1.f);
     if (p.w[k] && pl.on) {
       const float4* w = reinterpret_cast<const float4*>(p.w[k] + o);
-      const float4* v = reinterpret_cast<const float4*>(p.w[k] + o + p.d / 2);
+      const float4* v = reinterpret_cast<const float4*>(p.w[k] + o + D / 2);
       lo.a = w[0]; lo.b = w[1]; hi.a = v[0]; hi.b = v[1];
     }
     spread<HALF>(lo, hi, z);
   }
-  __device__ __forceinline__ Weights(const RopeArgs& args, const Place& place)
+  __device__ __forceinline__ Weights(const RopeArgs& args, const Place<D>& place)
       : p(args), pl(place), at(reinterpret_cast<ulonglong2*>(shared_base() + args.ring_bytes) + threadIdx.x) {
     if (!SHARED || p.norm == SVGEAR_QKNORM_NONE) return;
 #pragma unroll
@@ -247,18 +249,20 @@ struct Weights {
 // `table_tokens` tokens at once, so that every thread has a pair to compute; a
 // worker inside a warp fills its own token's.  Two buffers: one is filled again
 // only behind the barrier that follows the filling of the other.
+template <int D>
 struct Tables {
+  static constexpr int half = D / 2;
   float* base;
-  int half, left, buf, tok;
+  int left, buf, tok;
   __device__ __forceinline__ Tables(const RopeArgs& p, int slot)
       : base(reinterpret_cast<float*>(shared_base() + p.ring_bytes + p.weight_bytes)),
-        half(p.d / 2), left(0), buf(1), tok(0) {
-    if (p.tpt <= 32) base += slot * 2 * p.d;
+        left(0), buf(1), tok(0) {
+    if (p.tpt <= 32) base += slot * 2 * D;
   }
   __device__ __forceinline__ void next(const RopeArgs& p, const Token& t, int lane) {
     if (p.tpt <= 32) {
       buf ^= 1;
-      float* at = base + buf * p.d;
+      float* at = base + buf * D;
       for (int i = lane; i < half; i += p.tpt) {
         const float2 v = cos_sin(p, t.b, t.n, i);
         at[i] = v.x;
@@ -278,7 +282,7 @@ struct Tables {
         while (n >= p.N) { n -= p.N; ++b; }
         if (b < p.B) {
           const float2 v = cos_sin(p, b, n, i);
-          float* at = base + (buf * p.table_tokens + mine) * p.d;
+          float* at = base + (buf * p.table_tokens + mine) * D;
           at[i] = v.x;
           at[half + i] = v.y;
         }
@@ -288,7 +292,7 @@ struct Tables {
   }
   template <bool HALF>
   __device__ __forceinline__ void read(const RopeArgs& p, int j, f2 (&c)[4], f2 (&s)[4]) const {
-    const float* at = base + (p.tpt <= 32 ? buf : buf * p.table_tokens + tok) * p.d;
+    const float* at = base + (p.tpt <= 32 ? buf : buf * p.table_tokens + tok) * D;
     const int o0 = HALF ? j * 8 : j * 4, o1 = HALF ? j * 8 + 4 : half / 2 + j * 4;
     const ulonglong2 c0 = *reinterpret_cast<const ulonglong2*>(at + o0), c1 = *reinterpret_cast<const ulonglong2*>(at + o1);
     const ulonglong2 s0 = *reinterpret_cast<const ulonglong2*>(at + half + o0), s1 = *reinterpret_cast<const ulonglong2*>(at + half + o1);
@@ -300,10 +304,10 @@ struct Tables {
 // Token-major rows of up to OPS operands: workers inside a warp load them
 // straight into registers, one token ahead; blocks take them from a ring of
 // bulk copies in shared memory.
-template <typename T, int OPS>
+template <typename T, int OPS, int D>
 struct Direct {
   const RopeArgs& p;
-  const Place& pl;
+  const Place<D>& pl;
   Token ahead;
   int t;
   Raw<T> nx[OPS][2];
@@ -315,11 +319,11 @@ struct Direct {
       if (p.in[k] && t < pl.end && pl.on) {
         const T* x = static_cast<const T*>(p.in[k]) + ahead.b * p.batch[k] + ahead.n * p.ld[k] + pl.off;
         load_raw(nx[k][0], x);
-        load_raw(nx[k][1], x + p.d / 2);
+        load_raw(nx[k][1], x + D / 2);
       }
     }
   }
-  __device__ __forceinline__ Direct(const RopeArgs& args, const Place& place) : p(args), pl(place), ahead(args, place.t), t(place.t) { load(); }
+  __device__ __forceinline__ Direct(const RopeArgs& args, const Place<D>& place) : p(args), pl(place), ahead(args, place.t), t(place.t) { load(); }
   __device__ __forceinline__ void take(Raw<T> (&r)[OPS][2]) {
 #pragma unroll
     for (int k = 0; k < OPS; ++k) {
@@ -335,10 +339,10 @@ struct Direct {
 
 constexpr int kMaxStages = 8;
 
-template <typename T, int OPS>
+template <typename T, int OPS, int D>
 struct Ring {
   const RopeArgs& p;
-  const Place& pl;
+  const Place<D>& pl;
   Token ahead;       // the next token to be copied
   int t;
   uint32_t row;      // bytes of a token's row
@@ -362,8 +366,8 @@ struct Ring {
     ++t;
     ahead.step(p.N);
   }
-  __device__ __forceinline__ Ring(const RopeArgs& args, const Place& place)
-      : p(args), pl(place), ahead(args, place.t), t(place.t), row(args.H * args.d * sizeof(T)), slot(0), parity(0) {
+  __device__ __forceinline__ Ring(const RopeArgs& args, const Place<D>& place)
+      : p(args), pl(place), ahead(args, place.t), t(place.t), row(args.H * D * sizeof(T)), slot(0), parity(0) {
     __shared__ uint64_t bars[kMaxStages];
     __shared__ int flag;
     full = bars;
@@ -388,7 +392,7 @@ struct Ring {
     for (int k = 0; k < OPS; ++k) {
       if (p.in[k]) {
         r[k][0] = *reinterpret_cast<const Raw<T>*>(at + k * row);
-        r[k][1] = *reinterpret_cast<const Raw<T>*>(at + k * row + p.d / 2 * sizeof(T));
+        r[k][1] = *reinterpret_cast<const Raw<T>*>(at + k * row + D / 2 * sizeof(T));
       } else {
         zero_raw(r[k][0]);
         zero_raw(r[k][1]);
@@ -424,18 +428,18 @@ constexpr bool ahead_of(int cls) {
   return sizeof(T) == 2 && cls < 3;
 }
 
-template <typename T, bool AHEAD>
+template <typename T, bool AHEAD, int D>
 struct Gradients {
   static constexpr int kParts = sizeof(Raw<T>) / 16;
   const RopeArgs& p;
-  const Place& pl;
+  const Place<D>& pl;
   Token ahead;
   int t;
   uint32_t at;
   int slot;
   uint8_t* mem;
   __device__ __forceinline__ const T* source(int k, const Token& tk) const {
-    return static_cast<const T*>(p.grad[k]) + ((long long)(tk.b * p.H + pl.head) * p.out_tokens + tk.n) * p.d + pl.j * kVec;
+    return static_cast<const T*>(p.grad[k]) + ((long long)(tk.b * p.H + pl.head) * p.out_tokens + tk.n) * D + pl.j * kVec;
   }
   __device__ __forceinline__ void issue(int s) {
     if (t < pl.end && pl.on) {
@@ -447,14 +451,14 @@ struct Gradients {
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < kParts; ++i)
-              tc::cp_async16(at + (((s * 3 + k) * 2 + h) * kParts + i) * blockDim.x * 16, reinterpret_cast<const uint8_t*>(x + h * (p.d / 2)) + i * 16, 16);
+              tc::cp_async16(at + (((s * 3 + k) * 2 + h) * kParts + i) * blockDim.x * 16, reinterpret_cast<const uint8_t*>(x + h * (D / 2)) + i * 16, 16);
         }
     }
     tc::cp_async_commit();
     ++t;
     ahead.step(p.N);
   }
-  __device__ __forceinline__ Gradients(const RopeArgs& args, const Place& place, uint8_t* slots)
+  __device__ __forceinline__ Gradients(const RopeArgs& args, const Place<D>& place, uint8_t* slots)
       : p(args), pl(place), ahead(args, place.t), t(place.t), slot(0), mem(slots + threadIdx.x * 16) {
     at = tc::smem_u32(mem);
     if (AHEAD)
@@ -477,24 +481,24 @@ struct Gradients {
           for (int i = 0; i < kParts; ++i)
             r[i] = *reinterpret_cast<const uint4*>(mem + (((slot * 3 + k) * 2 + h) * kParts + i) * blockDim.x * 16);
         } else {
-          load_raw(g[k][h], source(k, tk) + h * (p.d / 2));
+          load_raw(g[k][h], source(k, tk) + h * (D / 2));
         }
       }
     if (AHEAD && ++slot == kAheadStages) slot = 0;
   }
 };
 
-template <typename T, bool HALF, int CLS>
+template <typename T, bool HALF, int CLS, int D>
 __global__ void __launch_bounds__(Class<CLS, false>::kMax, (Class<CLS, false>::kThreads / Class<CLS, false>::kMax))
     k_qkv_rope(const __grid_constant__ RopeArgs p) {
   __shared__ float2 scratch[64];
   RowSum<CLS == 0 ? -1 : CLS == 1 ? 2 : CLS == 2 ? 4 : 5> sum(scratch, p.tpt);
-  const Place pl = place(p);
-  const int half = p.d / 2;
-  const float inv_c = 1.f / (float)(p.norm == SVGEAR_QKNORM_TOKEN ? p.H * p.d : p.d);
-  const Weights<HALF, CLS != 3> w(p, pl);
-  Tables tables(p, pl.slot);
-  typename std::conditional<CLS == 0, Direct<T, 3>, Ring<T, 3>>::type rows(p, pl);
+  const Place<D> pl = place<D>(p);
+  constexpr int half = D / 2;
+  const float inv_c = 1.f / (float)(p.norm == SVGEAR_QKNORM_TOKEN ? p.H * D : D);
+  const Weights<HALF, CLS != 3, D> w(p, pl);
+  Tables<D> tables(p, pl.slot);
+  typename std::conditional<CLS == 0, Direct<T, 3, D>, Ring<T, 3, D>>::type rows(p, pl);
   Token tk(p, pl.t);
   for (int it = 0; it < p.chunk; ++it, tk.step(p.N)) {
     const bool live = pl.t + it < pl.end;
@@ -504,7 +508,7 @@ __global__ void __launch_bounds__(Class<CLS, false>::kMax, (Class<CLS, false>::k
     Raw<T> raw[3][2];
     rows.take(raw);
     const bool mine = live && pl.on;
-    const long long o = ((long long)(tk.b * p.H + pl.head) * p.out_tokens + tk.n) * p.d + pl.j * kVec;
+    const long long o = ((long long)(tk.b * p.H + pl.head) * p.out_tokens + tk.n) * D + pl.j * kVec;
     if (p.in[2] && mine) {
       T* out = static_cast<T*>(p.out[2]) + o;
       store_raw(out, raw[2][0]);
@@ -551,19 +555,19 @@ __global__ void __launch_bounds__(Class<CLS, false>::kMax, (Class<CLS, false>::k
 // Backward: g = the gradient turned back; with a norm, n = x inv, u = g w:
 //   dx = inv (u - n mean(u n)) = inv u - x inv^3 sum(u x) / C,  dw += g n,
 // so that sum(x^2) and sum(u x) of Q and of K share one barrier.
-template <typename T, bool HALF, int CLS>
+template <typename T, bool HALF, int CLS, int D>
 __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kThreads / Class<CLS, true>::kMax))
     k_qkv_rope_back(const __grid_constant__ RopeArgs p) {
   __shared__ float2 scratch[128];
   constexpr bool kAhead = ahead_of<T>(CLS);
   RowSum<CLS == 0 ? -1 : CLS == 1 ? 2 : CLS == 2 ? 4 : 5> sum(scratch, p.tpt);
-  const Place pl = place(p);
-  const int half = p.d / 2;
-  const float inv_c = 1.f / (float)(p.norm == SVGEAR_QKNORM_TOKEN ? p.H * p.d : p.d);
-  const Weights<HALF, CLS != 3> w(p, pl);
-  Tables tables(p, pl.slot);
-  typename std::conditional<CLS == 0, Direct<T, 2>, Ring<T, 2>>::type rows(p, pl);
-  Gradients<T, kAhead> grads(p, pl, shared_base() + p.grads_at);
+  const Place<D> pl = place<D>(p);
+  constexpr int half = D / 2;
+  const float inv_c = 1.f / (float)(p.norm == SVGEAR_QKNORM_TOKEN ? p.H * D : D);
+  const Weights<HALF, CLS != 3, D> w(p, pl);
+  Tables<D> tables(p, pl.slot);
+  typename std::conditional<CLS == 0, Direct<T, 2, D>, Ring<T, 2, D>>::type rows(p, pl);
+  Gradients<T, kAhead, D> grads(p, pl, shared_base() + p.grads_at);
   Token tk(p, pl.t);
   Sixteen dw[2];
 #pragma unroll
@@ -648,7 +652,7 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
   if (p.norm == SVGEAR_QKNORM_TOKEN) {
     if (has && pl.on)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) put<float, HALF>(p.part + ((size_t)worker * 2 + k) * p.H * p.d + pl.off, half, dw[k]);
+      for (int k = 0; k < 2; ++k) put<float, HALF>(p.part + ((size_t)worker * 2 + k) * p.H * D + pl.off, half, dw[k]);
     return;
   }
   // Per-head weights: add the heads of this worker, in a warp, then over its warps.
@@ -669,18 +673,18 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
   if (p.tpt <= 32) {
     if (has && pl.lane < pl.lanes)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) put<float, HALF>(p.part + ((size_t)worker * 2 + k) * p.d + pl.j * kVec, half, dw[k]);
+      for (int k = 0; k < 2; ++k) put<float, HALF>(p.part + ((size_t)worker * 2 + k) * D + pl.j * kVec, half, dw[k]);
     return;
   }
   float* red = reinterpret_cast<float*>(shared_base());  // [warps][d], over the ring, whose copies have all been taken
   for (int k = 0; k < 2; ++k) {
     __syncthreads();
-    if ((threadIdx.x & 31) < pl.lanes) put<float, HALF>(red + (threadIdx.x >> 5) * p.d + pl.j * kVec, half, dw[k]);
+    if ((threadIdx.x & 31) < pl.lanes) put<float, HALF>(red + (threadIdx.x >> 5) * D + pl.j * kVec, half, dw[k]);
     __syncthreads();
-    for (int i = threadIdx.x; i < p.d; i += blockDim.x) {
+    for (int i = threadIdx.x; i < D; i += blockDim.x) {
       float s = 0.f;
-      for (int v = 0; v < p.tpt / 32; ++v) s += red[v * p.d + i];
-      if (has) p.part[((size_t)worker * 2 + k) * p.d + i] = s;
+      for (int v = 0; v < p.tpt / 32; ++v) s += red[v * D + i];
+      if (has) p.part[((size_t)worker * 2 + k) * D + i] = s;
     }
   }
 }
@@ -769,7 +773,7 @@ RopeArgs rope_args(const svgear_rope_params* p, const float* wq, const float* wk
   a.w[1] = wk;
   a.pos = pos;
   a.pos_batch = p->pos_per_batch ? (long long)p->N * 3 : 0;
-  a.B = p->B; a.N = p->N; a.H = p->H; a.d = p->d;
+  a.B = p->B; a.N = p->N; a.H = p->H;
   a.out_tokens = p->out_tokens > 0 ? p->out_tokens : p->N;
   a.norm = p->norm;
   a.tpt = s.tpt;
@@ -797,9 +801,9 @@ RopeArgs rope_args(const svgear_rope_params* p, const float* wq, const float* wk
   return a;
 }
 
-template <typename T, bool HALF, int CLS>
+template <typename T, bool HALF, int CLS, int D>
 cudaError_t launch_class(const RopeArgs& a, const Shape& s, bool back, cudaStream_t st) {
-  const auto kernel = back ? k_qkv_rope_back<T, HALF, CLS> : k_qkv_rope<T, HALF, CLS>;
+  const auto kernel = back ? k_qkv_rope_back<T, HALF, CLS, D> : k_qkv_rope<T, HALF, CLS, D>;
   if (s.smem > 32 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem);
     if (e != cudaSuccess) return e;
@@ -809,19 +813,23 @@ cudaError_t launch_class(const RopeArgs& a, const Shape& s, bool back, cudaStrea
   return cudaGetLastError();
 }
 
-template <typename T, bool HALF>
+template <typename T, bool HALF, int D>
 cudaError_t launch_half(const RopeArgs& a, const Shape& s, bool back, cudaStream_t st) {
-  if (s.cls == 0) return launch_class<T, HALF, 0>(a, s, back, st);
-  if (s.cls == 1) return launch_class<T, HALF, 1>(a, s, back, st);
-  if (s.cls == 2) return launch_class<T, HALF, 2>(a, s, back, st);
-  return launch_class<T, HALF, 3>(a, s, back, st);
+  if (s.cls == 0) return launch_class<T, HALF, 0, D>(a, s, back, st);
+  if (s.cls == 1) return launch_class<T, HALF, 1, D>(a, s, back, st);
+  if (s.cls == 2) return launch_class<T, HALF, 2, D>(a, s, back, st);
+  return launch_class<T, HALF, 3, D>(a, s, back, st);
 }
 
 cudaError_t launch_rope(const RopeArgs& a, const Shape& s, const svgear_rope_params* p, bool back, cudaStream_t st) {
   if (!a.status) return cudaErrorInvalidValue;
   const bool half = p->pairing == SVGEAR_PAIR_HALF;
-  if (p->dtype == DT_F32) return half ? launch_half<float, true>(a, s, back, st) : launch_half<float, false>(a, s, back, st);
-  return half ? launch_half<bf16, true>(a, s, back, st) : launch_half<bf16, false>(a, s, back, st);
+  if (p->d == 128) {
+    if (p->dtype == DT_F32) return half ? launch_half<float, true, 128>(a, s, back, st) : launch_half<float, false, 128>(a, s, back, st);
+    return half ? launch_half<bf16, true, 128>(a, s, back, st) : launch_half<bf16, false, 128>(a, s, back, st);
+  }
+  if (p->dtype == DT_F32) return half ? launch_half<float, true, 64>(a, s, back, st) : launch_half<float, false, 64>(a, s, back, st);
+  return half ? launch_half<bf16, true, 64>(a, s, back, st) : launch_half<bf16, false, 64>(a, s, back, st);
 }
 
 }  // namespace

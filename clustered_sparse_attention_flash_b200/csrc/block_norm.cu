@@ -672,42 +672,51 @@ struct SumArgs {
 };
 
 constexpr int kSumLanes = 16;
+constexpr int kSumCols = 128;
 
-// Column sums of one group: 32 columns per block, the group's slots dealt to
+// Column sums of one group: 128 columns per block, the group's slots dealt to
 // 16 warps, their results added in warp order.
 __global__ void __launch_bounds__(32 * kSumLanes) k_group_sums(const __grid_constant__ NormArgs p, const __grid_constant__ SumArgs q) {
-  __shared__ float red[3][kSumLanes][33];
+  __shared__ float4 red[3][kSumLanes][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + lane;
+  const int col = blockIdx.x * kSumCols + lane * 4;
+  const size_t plane = (size_t)p.D;
   for (int g = blockIdx.y; g < p.G; g += gridDim.y) {
     const int beg = g ? group_end(p, g - 1) : 0, end = group_end(p, g);
-    float s[3] = {0.f, 0.f, 0.f};
-    if (end > beg && col < p.D) {
-      const long long c0 = beg / p.chunk + g, c1 = (end - 1) / p.chunk + g;
-      for (long long c = c0 + w; c <= c1; c += kSumLanes) {
-        const float* part = q.part + (size_t)c * 3 * p.D + col;
+    float4 s[3];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) s[k] += part[(size_t)k * p.D];
+    for (int k = 0; k < 3; ++k) s[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (end > beg && col < p.D) {
+      const int c1 = (end - 1) / p.chunk + g;
+#pragma unroll 2
+      for (int c = beg / p.chunk + g + w; c <= c1; c += kSumLanes) {
+        const float* part = q.part + (size_t)c * 3 * plane + col;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const float4 v = *reinterpret_cast<const float4*>(part + k * plane);
+          s[k].x += v.x; s[k].y += v.y; s[k].z += v.z; s[k].w += v.w;
+        }
       }
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) red[k][w][lane] = s[k];
     __syncthreads();
-    if (w == 0 && col < p.D) {
+    // one column per thread from here
+    const int at = blockIdx.x * kSumCols + threadIdx.x;
+    if (threadIdx.x < kSumCols && at < p.D) {
+      float t[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        s[k] = 0.f;
+      for (int k = 0; k < 3; ++k)
 #pragma unroll
-        for (int i = 0; i < kSumLanes; ++i) s[k] += red[k][i][lane];
-      }
-      const size_t at = (size_t)g * p.D + col;
-      const float wt = p.weight ? p.weight[col] : 1.f, b = p.bias ? p.bias[col] : 0.f;
-      if (q.dshift) q.dshift[at] = s[0];
-      if (q.dscale) q.dscale[at] = fmaf(wt, s[1], b * s[0]);
-      if (q.dgate) q.dgate[at] = p.post_weight ? p.post_weight[col] * s[2] : s[2];
+        for (int i = 0; i < kSumLanes; ++i) t[k] += reinterpret_cast<const float*>(red[k][i])[threadIdx.x];
+      const size_t o = (size_t)g * plane + at;
+      const float wt = p.weight ? p.weight[at] : 1.f, b = p.bias ? p.bias[at] : 0.f;
+      if (q.dshift) q.dshift[o] = t[0];
+      if (q.dscale) q.dscale[o] = fmaf(wt, t[1], b * t[0]);
+      if (q.dgate) q.dgate[o] = p.post_weight ? p.post_weight[at] * t[2] : t[2];
       if (q.sums)
 #pragma unroll
-        for (int k = 0; k < 3; ++k) q.sums[((size_t)g * 3 + k) * p.D + col] = s[k];
+        for (int k = 0; k < 3; ++k) q.sums[((size_t)g * 3 + k) * plane + at] = t[k];
     }
     __syncthreads();
   }
@@ -855,14 +864,13 @@ cudaError_t block_norm_back_run(const BlockNorm& b, void* ws, cudaStream_t st) {
   q.dweight = b.dweight; q.dbias = b.dbias; q.dpost_weight = b.dpost_weight;
   if (q.dweight || q.dbias || q.dpost_weight) q.sums = cv.take<float>((size_t)p.G * 3 * p.D);
   cudaError_t e = launch_typed(b, p, s, true, st);
-  const int cols = (p.D + 31) / 32;
   if (e == cudaSuccess && (q.dgate || q.dscale || q.dshift || q.sums)) {
-    k_group_sums<<<dim3(cols, std::min(p.G, 32768)), 32 * kSumLanes, 0, st>>>(p, q);
+    k_group_sums<<<dim3((p.D + kSumCols - 1) / kSumCols, std::min(p.G, 32768)), 32 * kSumLanes, 0, st>>>(p, q);
     note_launch();
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && q.sums) {
-    k_weight_sums<<<cols, 32 * kSumLanes, 0, st>>>(p, q);
+    k_weight_sums<<<(p.D + 31) / 32, 32 * kSumLanes, 0, st>>>(p, q);
     note_launch();
     e = cudaGetLastError();
   }

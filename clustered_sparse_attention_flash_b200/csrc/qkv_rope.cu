@@ -700,8 +700,10 @@ __global__ void __launch_bounds__(32 * kSumLanes) k_rope_weight_sums(const float
   float* out = blockIdx.y ? dwk : dwq;
   if (!out) return;
   float s = 0.f;
-  if (col < C)
+  if (col < C) {
+#pragma unroll 4
     for (long long i = w; i < workers; i += kSumLanes) s += part[((size_t)i * 2 + blockIdx.y) * C + col];
+  }
   red[w][lane] = s;
   __syncthreads();
   if (w == 0 && col < C) {

@@ -212,19 +212,13 @@ int svgear_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int M, int
   return cuda_status(mx_dequantize_run(codes, scales, M, K, Y, dtype, S(stream)));
 }
 
-size_t svgear_mx_product_workspace_size(int M, int N, int K) {
-  return check_product(M, N, K) ? 0 : mx_product_ws_bytes(M, N, K);
-}
-
 int svgear_mx_product(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes, const uint8_t* w_scales,
-                      const float* bias, int M, int N, int K, void* Y, void* ws, size_t ws_bytes, void* stream) {
+                      const float* bias, int M, int N, int K, void* Y, void* stream) {
   const int rc = check_product(M, N, K);
   if (rc) return rc;
   if (!a_codes || !a_scales || !w_codes || !w_scales || !Y) return SVGEAR_ERR_INVALID;
   if (!aligned16(a_codes, a_scales, w_codes, w_scales, bias, Y)) return SVGEAR_ERR_INVALID;
-  const size_t need = mx_product_ws_bytes(M, N, K);
-  if (need && (!ws || !aligned16(ws) || ws_bytes < need)) return SVGEAR_ERR_WORKSPACE;
-  return cuda_status(mx_product_run(a_codes, a_scales, w_codes, w_scales, bias, M, N, K, Y, ws, S(stream)));
+  return cuda_status(mx_product_run(a_codes, a_scales, w_codes, w_scales, bias, M, N, K, Y, S(stream)));
 }
 
 }  // extern "C"

@@ -101,9 +101,8 @@ cudaError_t mx_quantize_run(const void* X, int dtype, int M, int K, int head_d, 
                             cudaStream_t st);
 cudaError_t mx_dequantize_run(const uint8_t* codes, const uint8_t* scales, int M, int K, void* Y, int dtype,
                               cudaStream_t st);
-size_t mx_product_ws_bytes(int M, int N, int K);
 cudaError_t mx_product_run(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes, const uint8_t* w_scales,
-                           const float* bias, int M, int N, int K, void* Y, void* ws, cudaStream_t st);
+                           const float* bias, int M, int N, int K, void* Y, cudaStream_t st);
 
 // ---- TMA tensor maps (tma_host.cu)
 constexpr int kTmaMapBytes = 128;

@@ -713,14 +713,8 @@ cudaError_t launch_pair(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_
 
 }  // namespace
 
-size_t mx_product_ws_bytes(int M, int N, int K) {
-  (void)M; (void)N; (void)K;
-  return 0;
-}
-
 cudaError_t mx_product_run(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes, const uint8_t* w_scales,
-                           const float* bias, int M, int N, int K, void* Y, void* ws, cudaStream_t st) {
-  (void)ws;
+                           const float* bias, int M, int N, int K, void* Y, cudaStream_t st) {
   ProductArgs p{};
   p.a_scales = a_scales; p.w_scales = w_scales; p.bias = bias;
   p.Y = static_cast<bf16*>(Y);

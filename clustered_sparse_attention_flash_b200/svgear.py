@@ -124,8 +124,7 @@ _SIGS = {
     "svgear_qkv_rope_backward": (_I, [_P] * 8 + [_RP] + [_P] * 6 + [_SZ, _P]),
     "svgear_mx_quantize": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
     "svgear_mx_dequantize": (_I, [_P, _P, _I, _I, _P, _I, _P]),
-    "svgear_mx_product_workspace_size": (_SZ, [_I, _I, _I]),
-    "svgear_mx_product": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _SZ, _P]),
+    "svgear_mx_product": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -346,14 +345,10 @@ def svgear_mx_dequantize(codes, scales, M, K, Y, dtype, stream=None):
         _ptr(codes), _ptr(scales), M, K, _ptr(Y), dtype, _stream(stream)))
 
 
-def svgear_mx_product_workspace_size(M, N, K) -> int:
-    return lib().svgear_mx_product_workspace_size(M, N, K)
-
-
-def svgear_mx_product(a_codes, a_scales, w_codes, w_scales, bias, M, N, K, Y, ws, ws_bytes, stream=None):
+def svgear_mx_product(a_codes, a_scales, w_codes, w_scales, bias, M, N, K, Y, stream=None):
     _check("svgear_mx_product", lib().svgear_mx_product(
-        _ptr(a_codes), _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), _ptr(bias), M, N, K, _ptr(Y), _ptr(ws),
-        ws_bytes, _stream(stream)))
+        _ptr(a_codes), _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), _ptr(bias), M, N, K, _ptr(Y),
+        _stream(stream)))
 
 
 # ------------------------------------------------------- torch conveniences
@@ -691,28 +686,45 @@ def qkv_rope_backward(dQ, dK, dV, q=None, k=None, *, axes, grid=None, positions=
     return {"dq": rows[0], "dk": rows[1], "dv": rows[2], "dwq": dwq, "dwk": dwk}
 
 
+def _rows_of(x):
+    """(M, K, head_d) of rows [M, K] or of head-major [H, M, d]."""
+    if not x.is_cuda:
+        raise ValueError("x: device tensor expected")
+    if not x.is_contiguous():
+        raise ValueError("x: contiguous tensor expected")
+    shape = x.shape
+    if len(shape) == 2:
+        return shape[0], shape[1], 0
+    if len(shape) == 3:
+        return shape[1], shape[0] * shape[2], shape[2]
+    raise ValueError(f"x: [M, K] or [H, M, d] expected, got shape {tuple(shape)}")
+
+
+def _quantize(x, M, K, head_d, st):
+    import torch
+    codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
+    _check("svgear_mx_quantize", lib().svgear_mx_quantize(
+        x.data_ptr(), _code(x.dtype), M, K, head_d, codes.data_ptr(), scales.data_ptr(), st))
+    return codes, scales
+
+
+def _product(pa, psa, M, w_codes, w_scales, bias, dev, st):
+    import torch
+    N, K, u8 = w_codes.shape[0], w_codes.shape[1] * 2, torch.uint8
+    ptrs = (_want("w_codes", w_codes, u8, (N, K // 2), dev), _want("w_scales", w_scales, u8, (N, K // 32), dev),
+            _want("bias", bias, torch.float32, (N,), dev))
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    _check("svgear_mx_product", lib().svgear_mx_product(pa, psa, *ptrs, M, N, K, y.data_ptr(), st))
+    return y
+
+
 def mx_quantize(x, stream=None):
     """(codes [M, K/2], scales [M, K/32]), uint8, of x [M, K] or of the attention's head-major output
     [H, M, d] (K = H d), through svgear_mx_quantize."""
-    import torch
-    if not x.is_cuda:
-        raise ValueError("x: device tensor expected")
-    if x.dim() == 2:
-        (M, K), head_d = x.shape, 0
-    elif x.dim() == 3:
-        H, M, head_d = x.shape
-        K = H * head_d
-    else:
-        raise ValueError(f"x: [M, K] or [H, M, d] expected, got shape {tuple(x.shape)}")
-    if not x.is_contiguous():
-        raise ValueError("x: contiguous tensor expected")
-    dev = x.device
-    with _On(dev, stream) as st:
-        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=dev)
-        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
-        _check("svgear_mx_quantize", lib().svgear_mx_quantize(
-            x.data_ptr(), _code(x.dtype), M, K, head_d, codes.data_ptr(), scales.data_ptr(), st))
-    return codes, scales
+    M, K, head_d = _rows_of(x)
+    with _On(x.device, stream) as st:
+        return _quantize(x, M, K, head_d, st)
 
 
 def mx_dequantize(codes, scales, dtype=None, stream=None):
@@ -738,23 +750,18 @@ def mx_product(a_codes, a_scales, w_codes, w_scales, bias=None, stream=None):
         raise ValueError("a_codes: device tensor expected")
     if a_codes.dim() != 2 or w_codes.dim() != 2:
         raise ValueError("a_codes [M, K/2] and w_codes [N, K/2] expected")
-    M, N, K = a_codes.shape[0], w_codes.shape[0], w_codes.shape[1] * 2
-    dev, u8 = a_codes.device, torch.uint8
-    ptrs = (_want("a_codes", a_codes, u8, (M, K // 2), dev), _want("a_scales", a_scales, u8, (M, K // 32), dev),
-            _want("w_codes", w_codes, u8, (N, K // 2), dev), _want("w_scales", w_scales, u8, (N, K // 32), dev),
-            _want("bias", bias, torch.float32, (N,), dev))
+    M, K, dev = a_codes.shape[0], w_codes.shape[1] * 2, a_codes.device
+    pa = _want("a_codes", a_codes, torch.uint8, (M, K // 2), dev)
+    psa = _want("a_scales", a_scales, torch.uint8, (M, K // 32), dev)
     with _On(dev, stream) as st:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        need = lib().svgear_mx_product_workspace_size(M, N, K)
-        ws = workspace(need, dev) if need else None
-        _check("svgear_mx_product", lib().svgear_mx_product(
-            *ptrs, M, N, K, y.data_ptr(), None if ws is None else ws.data_ptr(), need, st))
-    return y
+        return _product(pa, psa, M, w_codes, w_scales, bias, dev, st)
 
 
 def mx_linear(x, w_codes, w_scales, bias=None, stream=None):
     """Y [M, N] bfloat16 = quantised x times W^T + bias: mx_quantize, then mx_product."""
-    if x.dim() == 2 and x.shape[1] != 2 * w_codes.shape[1]:
-        raise ValueError(f"x: {2 * w_codes.shape[1]} columns expected, got shape {tuple(x.shape)}")
-    codes, scales = mx_quantize(x, stream)
-    return mx_product(codes, scales, w_codes, w_scales, bias, stream)
+    M, K, head_d = _rows_of(x)
+    if w_codes.dim() != 2 or K != 2 * w_codes.shape[1]:
+        raise ValueError(f"x: {2 * w_codes.shape[-1]} columns expected, got {K}")
+    with _On(x.device, stream) as st:
+        codes, scales = _quantize(x, M, K, head_d, st)
+        return _product(codes.data_ptr(), scales.data_ptr(), M, w_codes, w_scales, bias, x.device, st)

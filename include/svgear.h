@@ -483,13 +483,10 @@ SVGEAR_API int svgear_mx_dequantize(const uint8_t* codes, const uint8_t* scales,
 /* Y[m][n] = sum_k A[m][k] W[n][k] + bias[n], Y [M][N] bfloat16: tokens A [M][K]
  * times weights W [N][K], both MXFP4 as above.  Products are exact, sums are
  * float32, rounded once; a NaN scale makes its row (column) of Y NaN.
- *   bias [N] float32 or NULL.  N a multiple of 8, K a multiple of 32.
- *   ws: svgear_mx_product_workspace_size(M, N, K) bytes (may be 0, then NULL
- *   will do). */
-SVGEAR_API size_t svgear_mx_product_workspace_size(int M, int N, int K);
+ *   bias [N] float32 or NULL.  N a multiple of 8, K a multiple of 32. */
 SVGEAR_API int svgear_mx_product(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
                       const uint8_t* w_scales, const float* bias, int M, int N, int K, void* Y,
-                      void* ws, size_t ws_bytes, void* stream);
+                      void* stream);
 
 #ifdef __cplusplus
 }

@@ -181,9 +181,7 @@ def test_product_of_nan_scales_and_untouched_memory():
     sa[3, 2], sw[130, 9] = 255, 255
     args = [t.cuda() for t in (a, sa, w, sw)]
     y = torch.full((M + 2, N), 7.0, dtype=BF, device="cuda")
-    need = sv.svgear_mx_product_workspace_size(M, N, K)
-    ws = sv.workspace(need)
-    sv.svgear_mx_product(*args, None, M, N, K, y, ws, ws.numel())
+    sv.svgear_mx_product(*args, None, M, N, K, y)
     assert torch.isnan(y[3]).all() and torch.isnan(y[:M, 130]).all() and (y[M:] == 7).all()
     rest = y[:M].clone()
     rest[3], rest[:, 130] = 0, 0
@@ -247,15 +245,13 @@ def test_refusals(L):
                      (dict(Y=None), INV), (dict(Y=A + 2), INV)):
         assert d(**kw) == code, kw
 
-    def p(M=4, N=64, K=64, b=A, Y=A, ac=A, as_=A, wc=A, ws_=A, ws=A, n=1 << 40):
-        return L.svgear_mx_product(ac, as_, wc, ws_, b, M, N, K, Y, ws, n, None)
+    def p(M=4, N=64, K=64, b=A, Y=A, ac=A, as_=A, wc=A, ws_=A):
+        return L.svgear_mx_product(ac, as_, wc, ws_, b, M, N, K, Y, None)
 
     for kw, code in ((dict(M=0), INV), (dict(N=0), INV), (dict(K=0), INV), (dict(K=40), UNS), (dict(N=12), UNS),
                      (dict(M=2 ** 27, N=2 ** 24, K=32), UNS), (dict(ac=None), INV), (dict(as_=None), INV), (dict(wc=None), INV),
                      (dict(ws_=None), INV), (dict(Y=None), INV), (dict(b=A + 4), INV), (dict(Y=A + 8), INV), (dict(wc=A + 2), INV)):
         assert p(**kw) == code, kw
-        if set(kw) <= {"M", "N", "K"}:
-            assert L.svgear_mx_product_workspace_size(kw.get("M", 4), kw.get("N", 64), kw.get("K", 64)) == 0
     with pytest.raises(ValueError, match="device tensor"):
         sv.mx_quantize(torch.zeros(2, 64))
 

@@ -415,14 +415,14 @@ struct Ring {
 template <int CLS, bool BACK>
 struct Class {
   static constexpr int kMax = CLS <= 1 ? 128 : CLS == 2 ? 384 : 1024;
-  static constexpr int kThreads = CLS == 0 ? (BACK ? 256 : 512) : CLS == 1 ? (BACK ? 384 : 640) : CLS == 2 ? (BACK ? 384 : 768) : 1024;
+  static constexpr int kThreads = CLS == 0 ? (BACK ? 256 : 512) : CLS == 1 ? (BACK ? 384 : 512) : CLS == 2 ? 384 : 1024;
 };
 
 // Gradients of Q, K and V of a token, head-major: each thread copies its own
 // vectors into its own slots of shared memory, two tokens ahead (as registers
 // they would spill), so no barrier is needed before it reads them back.
 // Without slots (float32 rows, wide blocks) they are loaded where they are used.
-constexpr int kAheadStages = 3;
+constexpr int kAheadStages = 2;
 template <typename T>
 constexpr bool ahead_of(int cls) {
   return sizeof(T) == 2 && cls < 3;
@@ -720,6 +720,10 @@ struct Shape {
 };
 
 constexpr int kSmemPerSm = 228 * 1024, kSmemPerBlock = 3072;  // 1 KB per block is the system's, the rest static arrays
+// What the rings of an SM's blocks hold together at most.  More than about 80 KB
+// in flight only queues reads before the writes and takes the L1 away
+// (float32, 40 heads, 32,768 tokens: 748 us with 180 KB, 685 us).
+constexpr int kRingPerSm = 92 * 1024;
 
 Shape rope_shape(const svgear_rope_params* p, bool back) {
   Shape s;
@@ -747,6 +751,7 @@ Shape rope_shape(const svgear_rope_params* p, bool back) {
   // The forward pass brings q, k and v through the ring, the backward pass q and k where a norm needs them.
   const int stage = s.cls == 0 ? 0 : (back ? (normed ? 2 : 0) : 3) * p->H * p->d * (p->dtype == DT_F32 ? 4 : 2);
   int blocks = std::max(1, std::min(threads / s.block, 8));
+  if (stage && !back) blocks = std::min(blocks, std::max(2, kRingPerSm / (2 * stage)));
   auto stages = [&]() { return stage ? (kSmemPerSm / blocks - kSmemPerBlock - fixed) / stage : 1; };
   while (stage && blocks > 1 && stages() < 2) --blocks;
   // As many workers as the SMs hold at once, each with a run of tokens.
@@ -755,7 +760,7 @@ Shape rope_shape(const svgear_rope_params* p, bool back) {
   s.chunk = (int)((tokens + want - 1) / want);
   s.workers = (tokens + s.chunk - 1) / s.chunk;
   s.grid = (int)((s.workers + per - 1) / per);
-  s.stages = std::max(1, std::min({stages(), kMaxStages, s.chunk}));
+  s.stages = std::max(1, std::min({stages(), kMaxStages, s.chunk, std::max(2, kRingPerSm / blocks / std::max(stage, 1))}));
   s.ring_bytes = s.stages * stage;
   s.grads_at = s.ring_bytes + front;
   s.smem = s.ring_bytes + fixed;

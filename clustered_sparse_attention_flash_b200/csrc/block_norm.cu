@@ -9,8 +9,8 @@
 // The per-column coefficients (1+s) w, b (1+s) + t and g w2 stay in registers
 // while consecutive rows belong to one group.
 //
-// A row is owned by a worker: 8, 16 or 32 lanes of a warp for D <= 256,
-// otherwise a whole block (two 8-element vectors per thread).  A worker walks a contiguous run of rows, so column sums of the
+// Rows are taken by workers: a warp takes one to four rows of up to 256 columns
+// side by side, a whole block one wider row (two 8-element vectors per thread).  A worker walks a contiguous run of rows, so column sums of the
 // backward pass stay in registers until the group or the run ends; partial
 // sums then go to slot (worker + group), which no other pair maps to because
 // both only grow along the rows, and are added in slot order: no atomics, the
@@ -195,7 +195,8 @@ struct Direct {
       : p(args), c(cols), end(last) {
     load(first);
   }
-  __device__ __forceinline__ void take(int row) {
+  // The row loaded last becomes the current one, `next` is loaded.
+  __device__ __forceinline__ void take(int next) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       x[v] = nx[v];
@@ -205,7 +206,7 @@ struct Direct {
         dh[v] = ndh[v];
       }
     }
-    load(row + 1);
+    load(next);
   }
   template <int K>
   __device__ __forceinline__ void read(Vec (&f)[V]) const {
@@ -295,20 +296,52 @@ struct Ring {
   }
 };
 
-// The worker of a thread and its rows, up to the last group's end.
+// The worker of a thread and its run of rows, up to the last group's end.  A
+// worker takes `step` rows at a time, this thread's being `sub` behind the
+// first; no step reaches over a group's end.
 struct Place {
-  int worker, row, end, lane;
+  int worker, row, end, lane, sub, step;
 };
+template <bool NARROW>
 __device__ __forceinline__ Place place(const NormArgs& p) {
   Place q;
-  const int slot = threadIdx.x / p.tpr;
-  q.worker = blockIdx.x * (blockDim.x / p.tpr) + slot;
-  q.lane = threadIdx.x - slot * p.tpr;
+  if (NARROW) {
+    q.worker = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    q.step = 32 / p.tpr;
+    q.sub = (threadIdx.x & 31) / p.tpr;
+    q.lane = threadIdx.x & (p.tpr - 1);
+  } else {
+    q.worker = blockIdx.x;
+    q.step = 1;
+    q.sub = 0;
+    q.lane = threadIdx.x;
+  }
   const long long first = (long long)q.worker * p.chunk;
   q.end = (int)min(first + p.chunk, (long long)group_end(p, p.G - 1));
   q.row = (int)min(first, (long long)p.N);
   return q;
 }
+
+// Steps through a run: `base` the first row of this step, `next` of the one
+// behind it, `g` the rows' group, which ends (for this run) at `stop`.
+struct Walk {
+  int base, next, stop, end, g, step;
+  __device__ __forceinline__ Walk(const NormArgs& p, const Place& pl)
+      : base(pl.row), next(pl.row), stop(pl.row), end(pl.end), g(pl.row < pl.end ? group_of(p, pl.row) : 0), step(pl.step) {}
+  __device__ __forceinline__ bool more() const { return base < end; }
+  // True when this step opens a group.
+  __device__ __forceinline__ bool open(const NormArgs& p) {
+    const bool fresh = base >= stop;
+    if (fresh) {
+      int e;
+      while ((e = group_end(p, g)) <= base && g + 1 < p.G) ++g;
+      stop = min(e, end);
+    }
+    next = min(base + step, stop);
+    return fresh;
+  }
+  __device__ __forceinline__ void advance() { base = next; }
+};
 
 // The coefficients of this thread's columns in group g: (1 + scale) weight,
 // bias (1 + scale) + shift (forward), gate post_weight.  Narrow rows keep them in
@@ -414,24 +447,19 @@ __global__ void __launch_bounds__(Class<CLS, false>::kMax, (Class<CLS, false>::k
   constexpr int V = Class<CLS, false>::kV;
   __shared__ float2 scratch[64];
   Sum<CLS> sum(scratch, p.tpr);
-  const Place pl = place(p);
+  const Place pl = place<CLS == 0>(p);
   Columns<V> c;
   c.init(p.D, p.tpr, pl.lane, sum);
-  typename std::conditional<CLS == 0, Direct<TX, TY, 2, V>, Ring<TX, TY, 2, V>>::type rows(p, c, pl.row, pl.end);
-  int g = pl.row < pl.end ? group_of(p, pl.row) : 0;
-  int gend = pl.row;  // the first row loads the coefficients
+  typename std::conditional<CLS == 0, Direct<TX, TY, 2, V>, Ring<TX, TY, 2, V>>::type rows(p, c, pl.row + pl.sub, pl.end);
+  Walk at(p, pl);
   // a sum over the block is the barrier behind which a stage is free
   const bool barrier = (p.y && p.post != SVGEAR_NORM_NONE) || (p.h && p.pre != SVGEAR_NORM_NONE);
   Coefficients<V, CLS != 0> k(p, c, coefficient_memory(p));
-  for (int it = 0; it < p.chunk; ++it) {
-    const int row = pl.row + it;
-    const bool live = row < pl.end;
-    if (p.tpr >= 32 && !live) break;  // uniform over the worker, which is whole warps
-    if (live && row >= gend) {
-      while ((gend = group_end(p, g)) <= row && g + 1 < p.G) ++g;
-      load_coefficients(p, g, c, k, true);
-    }
-    rows.take(row);
+  for (; at.more(); at.advance()) {
+    if (at.open(p)) load_coefficients(p, at.g, c, k, true);
+    const int row = at.base + pl.sub;
+    const bool live = CLS != 0 || row < at.stop;
+    rows.take(at.next + pl.sub);
     const long long out = (long long)row * p.D;
     Vec f[V], m[V];
     rows.template read<kX>(f);
@@ -543,36 +571,50 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
   constexpr int V = Class<CLS, true>::kV;
   __shared__ float2 scratch[128];
   Sum<CLS> sum(scratch, p.tpr);
-  const Place pl = place(p);
+  const Place pl = place<CLS == 0>(p);
   Columns<V> c;
   c.init(p.D, p.tpr, pl.lane, sum);
-  typename std::conditional<CLS == 0, Direct<TX, TY, 4, V>, Ring<TX, TY, 4, V>>::type rows(p, c, pl.row, pl.end);
-  int g = pl.row < pl.end ? group_of(p, pl.row) : 0;
-  int gend = pl.row;
+  typename std::conditional<CLS == 0, Direct<TX, TY, 4, V>, Ring<TX, TY, 4, V>>::type rows(p, c, pl.row + pl.sub, pl.end);
+  Walk at(p, pl);
   // Rows are read to the end of their iteration.  With four stages or more the
   // barrier in the next row's sum frees them; otherwise one at the end does.
   const bool late = p.dh && p.pre != SVGEAR_NORM_NONE && p.stages > 3;
   const f2 a = pair(p.y ? p.a : 1.f);
   Coefficients<V, CLS != 0> k(p, c, coefficient_memory(p));
   Vec s1[V], s2[V], su[V];
-  auto flush = [&]() {
+  auto flush = [&](int g) {
     float* part = p.part + (size_t)(pl.worker + g) * 3 * p.D;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (c.on[v]) {
+    for (int v = 0; v < V; ++v) {
+      if (CLS == 0) {  // the sums of the rows taken side by side
+        const auto across = [&](Vec& s) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float2 h = halves(s.v[i]);
+            for (int o = p.tpr; o < 32; o <<= 1) {
+              h.x += __shfl_xor_sync(0xffffffffu, h.x, o);
+              h.y += __shfl_xor_sync(0xffffffffu, h.y, o);
+            }
+            s.v[i] = pair(h.x, h.y);
+          }
+        };
+        across(s1[v]);
+        across(s2[v]);
+        across(su[v]);
+      }
+      if (c.on[v] && pl.sub == 0) {
         store_vec(part + c.col[v], s1[v]);
         store_vec(part + p.D + c.col[v], s2[v]);
         store_vec(part + 2 * p.D + c.col[v], su[v]);
       }
+    }
   };
-  for (int it = 0; it < p.chunk; ++it) {
-    const int row = pl.row + it;
-    const bool live = row < pl.end;
-    if (p.tpr >= 32 && !live) break;
-    if (live && row >= gend) {
-      if (it) flush();
-      while ((gend = group_end(p, g)) <= row && g + 1 < p.G) ++g;
-      load_coefficients(p, g, c, k, false);
+  int open = -1;  // the group whose sums are being taken
+  for (; at.more(); at.advance()) {
+    if (at.open(p)) {
+      if (open >= 0) flush(open);
+      open = at.g;
+      load_coefficients(p, at.g, c, k, false);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         fill(s1[v], 0.f);
@@ -580,7 +622,9 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
         fill(su[v], 0.f);
       }
     }
-    rows.take(row);
+    const int row = at.base + pl.sub;
+    const bool live = CLS != 0 || row < at.stop;
+    rows.take(at.next + pl.sub);
     const long long out = (long long)row * p.D;
     Vec n[V], R[V];
     float2 st_m = make_float2(0.f, 1.f);  // mean and 1/deviation of y
@@ -661,7 +705,7 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
       rows.release(row);
     }
   }
-  if (pl.row < pl.end) flush();
+  if (open >= 0) flush(open);
 }
 
 struct SumArgs {
@@ -781,18 +825,17 @@ Shape norm_shape(const svgear_norm_params* p, bool back) {
               : s.cls == 2 ? (back ? Class<2, true>::kThreads : Class<2, false>::kThreads)
                            : Class<3, true>::kThreads;
   }
-  const int per = s.block / s.tpr;
+  const int per = s.cls == 0 ? s.block / 32 : 1, step = s.cls == 0 ? 32 / s.tpr : 1;  // workers of a block, rows of a step
   const int stage = p->D * ((p->res_dtype == DT_F32 ? 4 : 2) + (p->dtype == DT_F32 ? 4 : 2)) * (back ? 2 : 1);
   const int coefs = 2 * p->D * (int)sizeof(float);
   // Blocks per SM: what the registers allow, as long as each has two stages.
   int blocks = std::max(1, std::min(threads / s.block, 8));
   auto stages = [&]() { return (kSmemPerSm / blocks - kSmemPerBlock - coefs) / stage; };
   while (s.cls != 0 && blocks > 1 && stages() < 2) --blocks;
-  // As many workers as the SMs hold at once; more would only add partial sums.
-  // The backward pass of narrow rows is held to 2,048 for the same reason.
-  long long want = std::min<long long>(N, 148LL * blocks * per);
-  if (back && s.cls == 0) want = std::min<long long>(want, 2048);
-  s.chunk = (int)((N + want - 1) / want);
+  // As many workers as the SMs hold at once, each with whole steps; more would
+  // only add partial sums.
+  const long long want = std::min<long long>((N + step - 1) / step, 148LL * blocks * per);
+  s.chunk = (int)(((N + want - 1) / want + step - 1) / step * step);
   s.workers = (N + s.chunk - 1) / s.chunk;
   s.grid = (int)((s.workers + per - 1) / per);
   s.stages = s.cls == 0 ? 0 : std::max(1, std::min({stages(), kMaxStages, s.chunk, std::max(blocks == 1 ? 3 : 2, kRingPerSm / blocks / stage)}));

@@ -47,25 +47,34 @@ struct RopeArgs {
   double freq[kMaxPairs];  // turns per position
 };
 
-// cos and sin of pair i of token (b, n); the identity where nothing turns.
-__device__ __forceinline__ float2 cos_sin(const RopeArgs& p, int b, int n, int i) {
+// Where a token sits on the three axes; `on`: it turns at all.
+struct Spot {
+  int x[3];
+  bool on;
+};
+__device__ __forceinline__ Spot spot(const RopeArgs& p, int b, int n) {
+  Spot s;
+  s.on = p.pos || n < p.vol;
+  if (p.pos) {
+    const int32_t* at = p.pos + (long long)b * p.pos_batch + (long long)n * 3;
+    s.x[0] = at[0]; s.x[1] = at[1]; s.x[2] = at[2];
+  } else {
+    const int q = (int)((unsigned)n / (unsigned)p.g2), t = (int)((unsigned)q / (unsigned)p.g1);
+    s.x[0] = t;
+    s.x[1] = q - t * p.g1;
+    s.x[2] = n - q * p.g2;
+  }
+  return s;
+}
+
+// cos and sin of pair i of a token; the identity where nothing turns.
+__device__ __forceinline__ float2 cos_sin(const RopeArgs& p, const Spot& s, int i) {
   float2 v = make_float2(1.f, 0.f);
-  if (i < p.pairs) {
-    const int ax = i < p.pairs0 ? 0 : i < p.pairs01 ? 1 : 2;
-    int x = 0;
-    bool turn = true;
-    if (p.pos) {
-      x = p.pos[(long long)b * p.pos_batch + (long long)n * 3 + ax];
-    } else if (n < p.vol) {
-      x = ax == 2 ? n % p.g2 : ax == 1 ? n / p.g2 % p.g1 : n / p.g2 / p.g1;
-    } else {
-      turn = false;
-    }
-    if (turn) {
-      double t = ((double)x + p.origin[ax]) * p.freq[i];
-      t -= rint(t);
-      sincospif(2.f * (float)t, &v.y, &v.x);
-    }
+  if (s.on && i < p.pairs) {
+    const bool a0 = i < p.pairs0, a1 = i < p.pairs01;
+    double t = ((double)(a0 ? s.x[0] : a1 ? s.x[1] : s.x[2]) + (a0 ? p.origin[0] : a1 ? p.origin[1] : p.origin[2])) * p.freq[i];
+    t -= rint(t);
+    sincospif(2.f * (float)t, &v.y, &v.x);
   }
   return v;
 }
@@ -263,8 +272,9 @@ struct Tables {
     if (p.tpt <= 32) {
       buf ^= 1;
       float* at = base + buf * D;
+      const Spot s = spot(p, t.b, t.n);
       for (int i = lane; i < half; i += p.tpt) {
-        const float2 v = cos_sin(p, t.b, t.n, i);
+        const float2 v = cos_sin(p, s, i);
         at[i] = v.x;
         at[half + i] = v.y;
       }
@@ -281,7 +291,7 @@ struct Tables {
         int b = t.b, n = t.n + mine;
         while (n >= p.N) { n -= p.N; ++b; }
         if (b < p.B) {
-          const float2 v = cos_sin(p, b, n, i);
+          const float2 v = cos_sin(p, spot(p, b, n), i);
           float* at = base + (buf * p.table_tokens + mine) * D;
           at[i] = v.x;
           at[half + i] = v.y;

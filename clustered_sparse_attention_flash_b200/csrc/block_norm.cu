@@ -804,10 +804,16 @@ struct Shape {
 };
 
 constexpr int kSmemPerSm = 228 * 1024, kSmemPerBlock = 2048;  // 1 KB per block is the system's, the rest static arrays
-// What the rings of an SM's blocks hold together at most.  More than about 80 KB
-// in flight only queues reads before the writes (65,536 x 2,048: 207 us
-// with 195 KB, 175 us with 64 KB).
-constexpr int kRingPerSm = 80 * 1024;
+// What the rings of an SM's blocks hold together.  Beyond about 80 KB more reads
+// in flight only delay the writes (share of the copy rate: bf16 65,536 x 2,048
+// with 64 / 96 / 195 KB 0.94 / 0.84 / 0.80; float32 40,000 x 2,048 with 64 / 96
+// KB 0.93 / 0.85; 80,000 x 1,024 with 64 / 80 KB 0.97 / 0.86).  So the blocks per
+// SM are those whose two stages stay within kBlocksRing, or as many as give
+// kThreadBytes / (bytes of an x and a y element) threads where those are
+// more (bf16 75,600 x 5,120 with one / two blocks 0.76 / 0.91), and deeper rings
+// stay within kRingPerSm.  The backward pass computes more for each byte.
+constexpr int kBlocksRing = 76 * 1024, kBlocksRingBack = 132 * 1024, kThreadBytes = 2048;
+constexpr int kRingPerSm = 88 * 1024;
 
 Shape norm_shape(const svgear_norm_params* p, bool back) {
   Shape s;
@@ -828,10 +834,16 @@ Shape norm_shape(const svgear_norm_params* p, bool back) {
   const int per = s.cls == 0 ? s.block / 32 : 1, step = s.cls == 0 ? 32 / s.tpr : 1;  // workers of a block, rows of a step
   const int stage = p->D * ((p->res_dtype == DT_F32 ? 4 : 2) + (p->dtype == DT_F32 ? 4 : 2)) * (back ? 2 : 1);
   const int coefs = 2 * p->D * (int)sizeof(float);
-  // Blocks per SM: what the registers allow, as long as each has two stages.
+  // Blocks per SM: what the registers allow, as long as each has two stages, and
+  // no more than kBlocksRing says unless the threads were too few to keep up.
   int blocks = std::max(1, std::min(threads / s.block, 8));
   auto stages = [&]() { return (kSmemPerSm / blocks - kSmemPerBlock - coefs) / stage; };
-  while (s.cls != 0 && blocks > 1 && stages() < 2) --blocks;
+  if (s.cls != 0) {
+    const int pair_bytes = (p->res_dtype == DT_F32 ? 4 : 2) + (p->dtype == DT_F32 ? 4 : 2);
+    const int enough = (kThreadBytes / pair_bytes + s.block - 1) / s.block;
+    blocks = std::min(blocks, std::max(enough, (back ? kBlocksRingBack : kBlocksRing) / (2 * stage)));
+    while (blocks > 1 && stages() < 2) --blocks;
+  }
   // As many workers as the SMs hold at once, each with whole steps; more would
   // only add partial sums.
   const long long want = std::min<long long>((N + step - 1) / step, 148LL * blocks * per);

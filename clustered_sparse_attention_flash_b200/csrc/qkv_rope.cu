@@ -734,6 +734,10 @@ constexpr int kSmemPerSm = 228 * 1024, kSmemPerBlock = 3072;  // 1 KB per block 
 // in flight only queues reads before the writes and takes the L1 away
 // (float32, 40 heads, 32,768 tokens: 748 us with 180 KB, 685 us).
 constexpr int kRingPerSm = 92 * 1024;
+// The forward pass takes no more blocks than hold two stages each in this (16
+// heads of 128, share of the copy rate with 3 / 4 blocks: 0.91 / 0.79; 12 heads
+// with 4 / 5: 0.86 / 0.79; 8 heads with 7 / 8: 0.85 / 0.77).
+constexpr int kBlocksRing = 85 * 1024;
 
 Shape rope_shape(const svgear_rope_params* p, bool back) {
   Shape s;
@@ -761,7 +765,7 @@ Shape rope_shape(const svgear_rope_params* p, bool back) {
   // The forward pass brings q, k and v through the ring, the backward pass q and k where a norm needs them.
   const int stage = s.cls == 0 ? 0 : (back ? (normed ? 2 : 0) : 3) * p->H * p->d * (p->dtype == DT_F32 ? 4 : 2);
   int blocks = std::max(1, std::min(threads / s.block, 8));
-  if (stage && !back) blocks = std::min(blocks, std::max(2, kRingPerSm / (2 * stage)));
+  if (stage && !back) blocks = std::min(blocks, std::max(2, kBlocksRing / (2 * stage)));
   auto stages = [&]() { return stage ? (kSmemPerSm / blocks - kSmemPerBlock - fixed) / stage : 1; };
   while (stage && blocks > 1 && stages() < 2) --blocks;
   // As many workers as the SMs hold at once, each with a run of tokens.

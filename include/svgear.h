@@ -339,7 +339,10 @@ SVGEAR_API int svgear_forward(const void* Q, const void* K, const void* V, const
  * with svgear_mx_* as the projections in 4 bits.  No counterpart in the
  * paper.  The conventions above hold, with these differences: row lengths
  * are as stated per call, and in-place use is as stated per call; any other
- * overlap of an output with an input is not allowed.
+ * overlap of an output with an input is not allowed.  Make the first call of
+ * each on a device outside stream capture (it looks up the status word and
+ * sets kernel attributes).  Results are the same bits on every call.  No call
+ * keeps anything for the next one; calls on different streams may overlap.
  * ======================================================================== */
 
 /* ---------------------------------------------------------------------------

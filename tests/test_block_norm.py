@@ -174,6 +174,11 @@ CASES = [
     dict(N=500, D=2560, with_y=False, pre="rms", affine=False, cuts=[0, 499], types=(F32, BF)),
     dict(N=64, D=512, pre="none", post="none", G=2),
     dict(N=200, D=1536, eps=0.5, post="rms", G=4),
+    dict(N=40, D=8192, types=(F32, F32), post="layer", cuts=[0, 13, 40]),
+    dict(N=700, D=4096, types=(F32, F32), pre="rms", cuts=[0, 1, 699, 700]),
+    dict(N=5003, D=24, cuts=[0, 2, 3, 3, 9, 2500, 2501, 5000], types=(F32, BF), post="rms"),
+    dict(N=3001, D=120, pre="rms", cuts=[0, 1500, 3001]),
+    dict(N=900, D=640, G=900, affine=False),
 ]
 
 

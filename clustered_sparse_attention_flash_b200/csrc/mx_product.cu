@@ -88,7 +88,10 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pitch, int 
 // (cta_group::2): each holds its own 128 features and half of the tokens, so
 // an SM reads 7 KB of codes per 64 elements of K where a tile of its own would
 // read 10 KB; the shared-memory port (written once by TMA, read once by the
-// MMA) is what bounds this kernel.  The even block issues the MMAs for both.
+// MMA) is what bounds this kernel, and the power limit: 75,600 x 15,360 x 5,120
+// takes 2.75 ms, 4.3 PFLOP/s, 0.67 of four times the measured bf16 burst rate, the
+// tensor pipe 64 % active at 1.6 of 1.965 GHz.  (One SM per tile of 128 x 192:
+// 3.47 ms.)  The even block issues the MMAs for both.
 //   warp 0       TMA: code tiles of 256 elements (128 bytes per row, 128-byte
 //                swizzle) into a ring of stages; both blocks' copies complete on
 //                the even block's barrier
@@ -100,7 +103,7 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pitch, int 
 //                costs about a thousand cycles (and would wait for the scale
 //                warps' loads in flight): hence warps of their own and the deep
 //                ring.  (75,600 x 15,360 x 5,120: 6.61 ms with the scale warps
-//                releasing, 4.15 ms with a ring of five stages, then see below.)
+//                releasing, 4.15 ms with a ring of five stages, 2.82 ms so.)
 //   warps 8-11   epilogue: accumulators + bias to bf16 through shared memory
 //                into coalesced rows; two accumulators, so that it runs beside
 //                the next tile's MMAs

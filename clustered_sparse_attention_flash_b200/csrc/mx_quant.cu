@@ -8,7 +8,9 @@
 // NaN or an infinity gets the NaN scale (255) and zero codes, so the fault
 // shows in everything computed from it.
 //
-// HBM-bound: x in, half a byte plus 1/32 byte per element out.
+// HBM-bound: x in, half a byte plus 1/32 byte per element out.  Measured on a
+// B200, 32,768 x 2,048 bf16: quantisation 30.4 us, 5.6 TB/s (0.85 of a plain
+// copy), dequantisation 27.8 us, 6.1 TB/s (0.93).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -113,8 +115,8 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize(const T* __restrict__ 
 }
 
 // Head-major X whose heads are 2^n vectors wide: a block takes kThreads / 2^n
-// tokens of kBatch neighbouring heads, so that it reads whole kilobytes
-// (2,048 x 32,768 in 43.9 us by rows; with this order see the launcher).
+// tokens of kBatch neighbouring heads, so that it reads whole kilobytes (32,768
+// tokens of 16 heads of 128: 43.9 us in the order of the rows, 30.4 us in this).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_mx_quantize_heads(const T* __restrict__ X, int M, int H, int log_vph,
                                                                 uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {

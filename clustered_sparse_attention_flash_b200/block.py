@@ -41,6 +41,14 @@ def attention_block(x, w: BlockWeights, H: int, *, Cq: int, Ck: int, iters: int,
     each).  ws is a workspace of svgear_workspace_size bytes to keep between calls.  Returns (r, h): the new
     residual stream and the normed, modulated input of the block's other half."""
     import torch
+    with torch.cuda.device(x.device):
+        return _attention_block(x, w, H, Cq, Ck, iters, rho, axes, grid, shift, scale, gate, next_shift, next_scale,
+                                offsets, init_q, init_k, ws, eps)
+
+
+def _attention_block(x, w, H, Cq, Ck, iters, rho, axes, grid, shift, scale, gate, next_shift, next_scale, offsets,
+                     init_q, init_k, ws, eps):
+    import torch
     N = x.shape[0]
     _, n = sv.block_norm(x, scale=scale, shift=shift, offsets=offsets, eps=eps, dtype=torch.bfloat16)
     d = w.qkv[0].shape[0] // (3 * H)

@@ -4,10 +4,9 @@
 //   r = a x + g m w2      (r = x without y)
 //   n = Q(r),  h = (n w + b)(1 + s) + t
 //
-// One pass: a row is loaded once into registers, its statistics are taken
-// there, and r and h leave from the same registers.  h is formed from the unrounded r.
-// The per-column coefficients (1+s) w, b (1+s) + t and g w2 stay in registers
-// while consecutive rows belong to one group.
+// One pass: a row is loaded once, its statistics are taken in registers, and r
+// and h leave from there; h is formed from the unrounded r.  The per-column
+// coefficients (1+s) w, b (1+s) + t and g w2 are formed once per group of a run.
 //
 // Rows are taken by workers: a warp takes one to four rows of up to 256 columns
 // side by side, a whole block one wider row (two 8-element vectors per thread).
@@ -356,10 +355,9 @@ struct Walk {
 
 // The coefficients of this thread's columns in group g: (1 + scale) weight,
 // bias (1 + scale) + shift (forward), gate post_weight.  Narrow rows keep them in
-// registers; wide rows keep two in shared memory, each thread its own columns,
-// and the forward pass the first in registers: as registers they would cost the second block per SM (or spill
-// to local memory, which has no L1 left beside the ring: 879 us against 632 at
-// 75,600 x 5,120).
+// registers; wide rows keep two of them in shared memory, each thread its own
+// columns: in registers they would cost a block per SM, or spill to local
+// memory (75,600 x 5,120: 632 us and 879 us, against 538 us).
 template <int V, bool SHARED>
 struct Coefficients;
 template <int V>
@@ -861,7 +859,8 @@ Shape norm_shape(const svgear_norm_params* p, bool back) {
   s.chunk = (int)(((N + want - 1) / want + step - 1) / step * step);
   s.workers = (N + s.chunk - 1) / s.chunk;
   s.grid = (int)((s.workers + per - 1) / per);
-  s.stages = s.cls == 0 ? 0 : std::max(1, std::min({stages(), kMaxStages, s.chunk, std::max(blocks == 1 ? 3 : 2, kRingPerSm / blocks / stage)}));
+  const int deep = std::max(blocks == 1 ? 3 : 2, kRingPerSm / blocks / stage);
+  s.stages = s.cls == 0 ? 0 : std::max(1, std::min({stages(), kMaxStages, s.chunk, deep}));
   s.ring_bytes = s.stages * stage;
   s.smem = s.cls == 0 ? 0 : s.ring_bytes + coefs;
   return s;

@@ -363,7 +363,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
       for (int b = 0; b < R; ++b) {
         const int m = r + b * 128;
-        x.v[b + 1] = more && m < TN && m0 + m < p.M ? load_scales(p.a_scales + (size_t)(m0 + m) * pitch, pitch, fu) : make_uint4(0, 0, 0, 0);
+        const bool there = more && m < TN && m0 + m < p.M;
+        x.v[b + 1] = there ? load_scales(p.a_scales + (size_t)(m0 + m) * pitch, pitch, fu) : make_uint4(0, 0, 0, 0);
       }
       if (++fu == units) {
         fu = 0;
@@ -621,7 +622,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           if (C > 1) part[(c + i) * kTF + f] = __uint_as_float(v[i]);
-          else if (c + i < rows && f0 + f < p.N) p.Y[(size_t)(m0 + c + i) * p.N + f0 + f] = __float2bfloat16_rn(__uint_as_float(v[i]) + bias);
+          else if (c + i < rows && f0 + f < p.N)
+            p.Y[(size_t)(m0 + c + i) * p.N + f0 + f] = __float2bfloat16_rn(__uint_as_float(v[i]) + bias);
         }
       }
     if (C > 1) {

@@ -182,7 +182,8 @@ static void quantize(const void* X, int M, int K, int head_d, uint32_t* codes, u
     k_mx_quantize_heads<T><<<dim3((M + rows - 1) / rows, (H + kBatch - 1) / kBatch), kThreads, 0, st>>>(x, M, H, log_vph, codes, scales);
   } else {
     const long long vecs = (long long)M * (K / kVec);
-    k_mx_quantize<T><<<(int)((vecs + kThreads * kBatch - 1) / (kThreads * kBatch)), kThreads, 0, st>>>(x, vecs, M, K / kVec, head_d, codes, scales);
+    const int grid = (int)((vecs + kThreads * kBatch - 1) / (kThreads * kBatch));
+    k_mx_quantize<T><<<grid, kThreads, 0, st>>>(x, vecs, M, K / kVec, head_d, codes, scales);
   }
   note_launch();
 }

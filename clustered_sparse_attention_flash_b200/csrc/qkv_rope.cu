@@ -339,7 +339,10 @@ struct Direct {
       }
     }
   }
-  __device__ __forceinline__ Direct(const RopeArgs& args, const Place<D>& place) : p(args), pl(place), ahead(args, place.t), t(place.t) { load(); }
+  __device__ __forceinline__ Direct(const RopeArgs& args, const Place<D>& place)
+      : p(args), pl(place), ahead(args, place.t), t(place.t) {
+    load();
+  }
   __device__ __forceinline__ void take(Raw<T> (&r)[OPS][2]) {
 #pragma unroll
     for (int k = 0; k < OPS; ++k) {
@@ -467,7 +470,8 @@ struct Gradients {
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < kParts; ++i)
-              tc::cp_async16(at + (((s * 3 + k) * 2 + h) * kParts + i) * blockDim.x * 16, reinterpret_cast<const uint8_t*>(x + h * (D / 2)) + i * 16, 16);
+              tc::cp_async16(at + (((s * 3 + k) * 2 + h) * kParts + i) * blockDim.x * 16,
+                             reinterpret_cast<const uint8_t*>(x + h * (D / 2)) + i * 16, 16);
         }
     }
     tc::cp_async_commit();
@@ -735,7 +739,7 @@ struct Shape {
   long long workers;
 };
 
-constexpr int kSmemPerSm = 228 * 1024, kSmemPerBlock = 3072;  // 1 KB per block is the system's, the rest static arrays
+constexpr int kSmemPerSm = 228 * 1024, kSmemPerBlock = 3 * 1024;  // 1 KB per block is the system's, the rest static arrays
 // What the rings of an SM's blocks hold together at most.  More than about 80 KB
 // in flight only queues reads before the writes and takes the L1 away
 // (float32, 40 heads, 32,768 tokens: 748 us with 180 KB, 685 us).

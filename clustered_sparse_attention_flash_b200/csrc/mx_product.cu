@@ -84,14 +84,18 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pitch, int 
 
 // ------------------------------------------------------------- many tokens
 //
-// Two neighbouring SMs work on one tile of 256 features x 192 tokens
+// Two neighbouring SMs work on one tile of 256 features x TN tokens
 // (cta_group::2): each holds its own 128 features and half of the tokens, so
-// an SM reads 7 KB of codes per 64 elements of K where a tile of its own would
-// read 10 KB; the shared-memory port (written once by TMA, read once by the
-// MMA) is what bounds this kernel, and the power limit: 75,600 x 15,360 x 5,120
-// takes 2.75 ms, 4.3 PFLOP/s, 0.67 of four times the measured bf16 burst rate, the
-// tensor pipe 64 % active at 1.6 of 1.965 GHz.  (One SM per tile of 128 x 192:
-// 3.47 ms.)  The even block issues the MMAs for both.
+// that at TN = 192 an SM reads 7 KB of codes per 64 elements of K where a tile of
+// its own would read 10 KB.  What bounds it is the shared-memory port, which each
+// code passes once from TMA and once to the MMA, and the power limit: 75,600 x
+// 15,360 x 5,120 of quantised normal data takes 2.53 ms at TN = 224, 4.7 PFLOP/s,
+// 0.73 of four times the measured bf16 burst rate; with zeros for data, which
+// take less power, 5.6 PFLOP/s.  (TN = 192: 2.72 ms and 5.0 PFLOP/s; one SM per
+// tile of 128 x 192: 3.47 ms.)  Beside two accumulators of 224 tokens tensor
+// memory holds the scales of two stages, so that a stage's scales wait for the
+// MMAs two stages back; at 192 each stage of the ring has its own.  The launcher
+// chooses by the rounds of tiles.  The even block issues the MMAs for both.
 //   warp 0       TMA: code tiles of 256 elements (128 bytes per row, 128-byte
 //                swizzle) into a ring of stages; both blocks' copies complete on
 //                the even block's barrier
@@ -109,18 +113,19 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pitch, int 
 //                the next tile's MMAs
 
 constexpr int kPairThreads = 384;
-constexpr int kPairTokens = 192;
 
+template <int TN>
 struct Pair {
   static constexpr int kTokBlocks = 2;                             // 128-row scale atoms of the tokens
-  static constexpr int kCodesF = kTF * 128, kCodesT = kPairTokens / 2 * 128, kCodes = kCodesF + kCodesT;
+  static constexpr int kCodesF = kTF * 128, kCodesT = TN / 2 * 128, kCodes = kCodesF + kCodesT;
   static constexpr int kSfF = 2 * 512, kSf = kSfF + 2 * 512 * kTokBlocks;  // scales of a stage
   static constexpr int kStages = 5, kUnits = 8;
   static constexpr int kOut = 2 * kChunk * kTF * 2;                // two staging buffers, bf16
   static constexpr int kBars = 512;
   static constexpr int kSmem = kStages * kCodes + kUnits * 2 * kSf + kOut + kBars + 1024;
   static constexpr int kSfCols = 8 + 8 * kTokBlocks;               // per stage: 2 atoms of features, 2 of each token block
-  static_assert(2 * kPairTokens + kStages * kSfCols <= 512 && kSmem <= kSmemLimit && kCodes % 1024 == 0, "tile does not fit");
+  static constexpr int kSfSlots = TN <= 192 ? kStages : 2;         // of tensor memory
+  static_assert(2 * TN + kSfSlots * kSfCols <= 512 && kSmem <= kSmemLimit && kCodes % 1024 == 0, "tile does not fit");
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -206,10 +211,11 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       : "memory");
 }
 
+template <int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_mx_pair(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, const ProductArgs p) {
-  using T = Pair;
-  constexpr int S = T::kStages, U = T::kUnits, TN = kPairTokens;
+  using T = Pair<TN>;
+  constexpr int S = T::kStages, U = T::kUnits;
   extern __shared__ uint8_t smem_raw[];
   // the dynamic part starts at the same offset in both blocks, and so does all of this
   uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -296,11 +302,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int s = it % S, u = un % U, h = kb & 1;  // a unit's two stages
         if (h == 0) ok = wait_cluster(sf_full + u, un / U & 1, abort_flag, p.status);
         ok = ok && tc::mbar_wait_warp(codes_full + s, it / S & 1, abort_flag, p.status);
+        // the MMAs that read this stage's scale slot before (with a slot per stage they are known to be done)
+        if (T::kSfSlots < S && ok && it >= T::kSfSlots) {
+          const uint32_t back = it - T::kSfSlots;
+          ok = tc::mbar_wait_warp(empty + back % S, back / S & 1, abort_flag, p.status);
+        }
         if (!ok) break;
         tc::tc_fence_after();
         const uint32_t wf = tc::smem_u32(codes_s + s * T::kCodes), tk = wf + T::kCodesF;
         const uint32_t sf = tc::smem_u32(sf_s + (u * 2 + h) * T::kSf);
-        const uint32_t tf = tmem + 2 * TN + s * T::kSfCols, tt = tf + 8;
+        const uint32_t tf = tmem + 2 * TN + it % T::kSfSlots * T::kSfCols, tt = tf + 8;
         const bool last = kb + 1 == p.kblocks;
         if (leader) {
 #pragma unroll
@@ -703,17 +714,25 @@ cudaError_t launch_few(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_c
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+template <int TN>
 cudaError_t launch_pair(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_codes, cudaStream_t st) {
+  using T = Pair<TN>;
   CUtensorMap map_w, map_a;
-  if (!tma_map_u8_rows(&map_w, w_codes, p.K / 2, p.N, kTF) || !tma_map_u8_rows(&map_a, a_codes, p.K / 2, p.M, kPairTokens / 2))
+  if (!tma_map_u8_rows(&map_w, w_codes, p.K / 2, p.N, kTF) || !tma_map_u8_rows(&map_a, a_codes, p.K / 2, p.M, TN / 2))
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(k_mx_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, Pair::kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(k_mx_pair<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
   if (e != cudaSuccess) return e;
   p.ftiles = (p.N + 2 * kTF - 1) / (2 * kTF);
-  p.tiles = p.ftiles * ((p.M + kPairTokens - 1) / kPairTokens);
-  k_mx_pair<<<2 * std::min(p.tiles, 74), kPairThreads, Pair::kSmem, st>>>(map_w, map_a, p);
+  p.tiles = p.ftiles * ((p.M + TN - 1) / TN);
+  k_mx_pair<TN><<<2 * std::min(p.tiles, 74), kPairThreads, T::kSmem, st>>>(map_w, map_a, p);
   note_launch();
   return cudaGetLastError();
+}
+
+// Rounds of tiles that 74 pairs of SMs take.
+long long pair_rounds(int M, int N, int TN) {
+  const long long tiles = (long long)((N + 2 * kTF - 1) / (2 * kTF)) * ((M + TN - 1) / TN);
+  return (tiles + 73) / 74;
 }
 
 }  // namespace
@@ -730,7 +749,13 @@ cudaError_t mx_product_run(const uint8_t* a_codes, const uint8_t* a_scales, cons
   if (M <= 16) return launch_few<16>(p, a_codes, w_codes, st);
   // From 65 tokens on the wide tiles win even where they leave SMs idle.
   if (M <= 64) return launch_few<64>(p, a_codes, w_codes, st);
-  return launch_pair(p, a_codes, w_codes, st);
+  // A round of 224 tokens takes 1.05 to 1.12 times a round of 192 (1,000 x 5,120 x
+  // 5,120: 24.0 against 21.7 us for two rounds), so it has to save 3 rounds in 23:
+  // 16,384 x 2,048 x 2,048 takes 42 us in 8 rounds of 224 and 50 in 10 of 192,
+  // 200 x 15,360 x 5,120 17.4 in one and 21.3 in two, 75,600 x 15,360 x 5,120 2.53
+  // ms and 2.72; 6,000 x 5,120 x 5,120, 8 rounds against 9, takes 75 and 74 us.
+  return 20 * pair_rounds(M, N, 192) > 23 * pair_rounds(M, N, 224) ? launch_pair<224>(p, a_codes, w_codes, st)
+                                                                   : launch_pair<192>(p, a_codes, w_codes, st);
 }
 
 }  // namespace svg

@@ -20,7 +20,7 @@ inline int esize(int dtype) { return dtype == SVGEAR_BF16 ? 2 : 4; }
 
 constexpr int kMaxNormCols = 8192;
 constexpr int kMaxTokenCols = 16384;
-constexpr int kMaxRows = 1 << 30;  // row counters are int, and run ahead by a few stages
+constexpr int kMaxRows = 1 << 30;  // row counters are int, and run ahead by a few stages or a tile
 
 int check_norm(const svgear_norm_params* p) {
   if (!p || p->N < 1 || p->D < 1 || p->G < 1) return SVGEAR_ERR_INVALID;
@@ -87,7 +87,7 @@ int check_rope_inputs(const void* const in[3], const float* wq, const float* wk,
 
 int check_mx(int M, int K) {
   if (M < 1 || K < 1) return SVGEAR_ERR_INVALID;
-  if (K % 32 || K > (1 << 20)) return SVGEAR_ERR_UNSUPPORTED;
+  if (K % 32 || K > (1 << 20) || M > kMaxRows) return SVGEAR_ERR_UNSUPPORTED;
   if ((long long)M * K >= (1LL << 39)) return SVGEAR_ERR_UNSUPPORTED;  // one block of 2,048 elements per grid index
   return SVGEAR_OK;
 }

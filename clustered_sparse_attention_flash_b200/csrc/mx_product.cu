@@ -11,8 +11,8 @@
 // Scales lie as plain rows in global memory.  A warpgroup brings them into the
 // tensor core's order in shared memory (an atom of 128 rows x 4 scales is 512
 // bytes, row r at 16 (r mod 32) + 4 (r div 32)), from where tcgen05.cp takes
-// them to tensor memory.  They keep one tensor-memory slot per ring stage: a
-// slot is written again only after the MMAs that read it have committed.
+// them to tensor memory, into a slot that is written again only after the MMAs
+// that read it have committed.
 #include <cuda.h>
 
 #include <algorithm>
@@ -103,11 +103,12 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pitch, int 
 //   warps 4-7    scales of the block's features and of all the tile's tokens, in
 //                units of two stages and a ring of their own, eight units deep
 //   warps 1-3    in the odd block: pass the word that an accumulator has been
-//                read (1) or a unit is there (2, 3) on to the even block.  The release over the cluster that this takes
-//                costs about a thousand cycles (and would wait for the scale
-//                warps' loads in flight): hence warps of their own and the deep
-//                ring.  (75,600 x 15,360 x 5,120: 6.61 ms with the scale warps
-//                releasing, 4.15 ms with a ring of five stages, 2.82 ms so.)
+//                read (1) or a unit is there (2, 3) on to the even block.  The
+//                release over the cluster that this takes costs about a thousand
+//                cycles (and would wait for the scale warps' loads in flight):
+//                hence warps of their own and the deep ring.  (75,600 x 15,360 x
+//                5,120: 6.61 ms with the scale warps releasing, 4.15 ms with a
+//                ring of five stages, 2.82 ms so.)
 //   warps 8-11   epilogue: accumulators + bias to bf16 through shared memory
 //                into coalesced rows; two accumulators, so that it runs beside
 //                the next tile's MMAs

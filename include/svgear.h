@@ -466,7 +466,8 @@ SVGEAR_API int svgear_qkv_rope_backward(const void* dQ, const void* dK, const vo
  * consecutive elements of a row, E2M1 elements under one E8M0 scale
  * 2^(byte-127).
  *   codes [M][K/2]: two elements per byte, the even one in the low four bits;
- *   scales [M][K/32] bytes.  K a multiple of 32.
+ *   scales [M][K/32] bytes.  K a multiple of 32, at most 2^20; M at most 2^30,
+ *   M K below 2^39.
  * Quantisation (section 6.3 of the specification): scale exponent
  * floor(log2 amax) - 2 clamped to the format's range, elements rounded to
  * nearest even, magnitudes above 6 scales saturate.  A block that holds a NaN
@@ -486,7 +487,7 @@ SVGEAR_API int svgear_mx_dequantize(const uint8_t* codes, const uint8_t* scales,
 /* Y[m][n] = sum_k A[m][k] W[n][k] + bias[n], Y [M][N] bfloat16: tokens A [M][K]
  * times weights W [N][K], both MXFP4 as above.  Products are exact, sums are
  * float32, rounded once; a NaN scale makes its row (column) of Y NaN.
- *   bias [N] float32 or NULL.  N a multiple of 8, K a multiple of 32. */
+ *   bias [N] float32 or NULL.  N a multiple of 8, at most 2^30; M, K as above. */
 SVGEAR_API int svgear_mx_product(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
                       const uint8_t* w_scales, const float* bias, int M, int N, int K, void* Y,
                       void* stream);

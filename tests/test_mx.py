@@ -257,6 +257,17 @@ def test_refusals(L):
         sv.mx_quantize(torch.zeros(2, 64))
 
 
+def test_refusals_of_row_counts(L):
+    """Row counters run up to a tile beyond the last row and stay below 2^31."""
+    UNS = sv.SVGEAR_ERR_UNSUPPORTED
+    for M in (2 ** 30 + 1, 2 ** 31 - 1):
+        assert L.svgear_mx_quantize(A, 1, M, 32, 0, A, A, None) == UNS
+        assert L.svgear_mx_dequantize(A, A, M, 32, A, 1, None) == UNS
+        assert L.svgear_mx_product(A, A, A, A, None, M, 8, 32, A, None) == UNS
+    for N in (2 ** 30 + 8, 2 ** 31 - 8):
+        assert L.svgear_mx_product(A, A, A, A, None, 4, N, 32, A, None) == UNS
+
+
 @pytest.mark.gpu
 def test_refusals_of_tensors():
     x = torch.zeros(4, 64, device="cuda")

@@ -17,6 +17,7 @@
 
 #include <algorithm>
 
+#include "chain.cuh"
 #include "internal.h"
 #include "tc_common.cuh"
 
@@ -214,9 +215,10 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
 
 template <int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    k_mx_pair(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, const ProductArgs p) {
+    k_mx_pair(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, const ProductArgs args) {
   using T = Pair<TN>;
   constexpr int S = T::kStages, U = T::kUnits;
+  ProductArgs p = args;
   extern __shared__ uint8_t smem_raw[];
   // the dynamic part starts at the same offset in both blocks, and so does all of this
   uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -266,6 +268,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync();  // both blocks' barriers are there, and their tensor memory
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_previous(p.a_scales, p.w_scales, p.bias, p.Y);
 
   if (warp == 0) {
     // ------------------------------------------------------- code tiles
@@ -496,9 +499,10 @@ __device__ __forceinline__ uint2 load_scales8(const uint8_t* row, int pitch, int
 
 template <int TN>
 __global__ void __launch_bounds__(kFewThreads, 2)
-    k_mx_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, const ProductArgs p, int C) {
+    k_mx_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, const ProductArgs args, int C) {
   using T = FewTile<TN>;
   constexpr int S = T::kStages;
+  ProductArgs p = args;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* codes_s = smem;
@@ -536,6 +540,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_previous(p.a_scales, p.w_scales, p.bias, p.Y);
 
   if (warp == 0) {
     // ------------------------------------------------------- code tiles
@@ -693,26 +698,14 @@ cudaError_t launch_few(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_c
   CUtensorMap map_w, map_a;
   if (!tma_map_u8_rows(&map_w, w_codes, p.K / 2, p.N, kTF) || !tma_map_u8_rows(&map_a, a_codes, p.K / 2, p.M, TN))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(k_mx_few<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(k_mx_few<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
   if (e != cudaSuccess) return e;
   p.ftiles = (p.N + kTF - 1) / kTF;
   p.tiles = p.ftiles * ((p.M + TN - 1) / TN);
   int C = 1;
   while (C < 8 && p.tiles * C * 2 <= 160 && p.kblocks >= 4 * C) C *= 2;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.tiles * C);
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = T::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = C;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k_mx_few<TN>, map_w, map_a, p, C);
   note_launch();
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  return launch_chained(k_mx_few<TN>, p.tiles * C, kFewThreads, T::kSmem, C, st, map_w, map_a, p, C);
 }
 
 template <int TN>
@@ -725,9 +718,8 @@ cudaError_t launch_pair(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_
   if (e != cudaSuccess) return e;
   p.ftiles = (p.N + 2 * kTF - 1) / (2 * kTF);
   p.tiles = p.ftiles * ((p.M + TN - 1) / TN);
-  k_mx_pair<TN><<<2 * std::min(p.tiles, 74), kPairThreads, T::kSmem, st>>>(map_w, map_a, p);
   note_launch();
-  return cudaGetLastError();
+  return launch_chained(k_mx_pair<TN>, 2 * std::min(p.tiles, 74), kPairThreads, T::kSmem, 0, st, map_w, map_a, p);
 }
 
 // Rounds of tiles that 74 pairs of SMs take.

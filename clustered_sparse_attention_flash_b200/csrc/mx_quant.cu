@@ -13,6 +13,7 @@
 // copy), dequantisation 27.8 us, 6.1 TB/s (0.93).
 #include <cuda_fp16.h>
 
+#include "chain.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "rowvec.cuh"
@@ -84,6 +85,7 @@ __device__ __forceinline__ uint32_t quantise(float (&f)[kVec], uint32_t& byte) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_mx_quantize(const T* __restrict__ X, long long vecs, int M, int vpr, int head_d,
                                                           uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  launch_next();
   const long long base = (long long)blockIdx.x * (kThreads * kBatch);
   const long long row0 = base / vpr;  // one 64-bit division per block
   const uint32_t in0 = (uint32_t)(base - row0 * vpr) + threadIdx.x;
@@ -120,6 +122,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize(const T* __restrict__ 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_mx_quantize_heads(const T* __restrict__ X, int M, int H, int log_vph,
                                                                 uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  launch_next();
   const int vph = 1 << log_vph, vec = threadIdx.x & (vph - 1);
   const long long row = (long long)blockIdx.x * (kThreads >> log_vph) + (threadIdx.x >> log_vph);
   const int h0 = blockIdx.y * kBatch;

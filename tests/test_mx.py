@@ -222,6 +222,38 @@ def test_same_bits_on_another_stream_and_in_two_graphs(M):
     del graphs
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_linears_in_a_row(M):
+    """Each call reads what the one before has just written, and its memory is taken again: the same bits as with
+    a pause after every call, eagerly and in a replayed graph."""
+    K = 1024
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).cuda().bfloat16()
+    ws = [tuple(t.cuda() for t in weights(K, K, i)) for i in range(3)]
+
+    def chain(pause):
+        y = x
+        for i in range(12):
+            y = sv.mx_linear(y, *ws[i % 3])
+            y = y / y.float().abs().amax().clamp(min=1e-3).bfloat16() if i % 4 == 3 else y
+            if pause:
+                torch.cuda.synchronize()
+        return y
+
+    want = chain(True)
+    assert want.isfinite().all() and want.count_nonzero() > 0
+    assert all(torch.equal(chain(False), want) for _ in range(5))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        y = chain(False)
+    for _ in range(3):
+        y.zero_()
+        graph.replay()
+        assert torch.equal(y, want)
+
+
 # ------------------------------------------------------------------ refusals
 
 @pytest.fixture(scope="module")

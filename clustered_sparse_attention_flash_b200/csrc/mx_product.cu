@@ -95,8 +95,9 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pitch, int 
 // take less power, 5.6 PFLOP/s.  (TN = 192: 2.72 ms and 5.0 PFLOP/s; one SM per
 // tile of 128 x 192: 3.47 ms.)  Beside two accumulators of 224 tokens tensor
 // memory holds the scales of two stages, so that a stage's scales wait for the
-// MMAs two stages back; at 192 each stage of the ring has its own.  The launcher
-// chooses by the rounds of tiles.  The even block issues the MMAs for both.
+// MMAs two stages back; narrower tiles have a slot for each stage of the ring.
+// The launcher chooses by the rounds of tiles.  The even block issues the MMAs
+// for both.
 //   warp 0       TMA: code tiles of 256 elements (128 bytes per row, 128-byte
 //                swizzle) into a ring of stages; both blocks' copies complete on
 //                the even block's barrier
@@ -118,10 +119,10 @@ constexpr int kPairThreads = 384;
 
 template <int TN>
 struct Pair {
-  static constexpr int kTokBlocks = 2;                             // 128-row scale atoms of the tokens
+  static constexpr int kTokBlocks = TN > 128 ? 2 : 1;              // 128-row scale atoms of the tokens
   static constexpr int kCodesF = kTF * 128, kCodesT = TN / 2 * 128, kCodes = kCodesF + kCodesT;
   static constexpr int kSfF = 2 * 512, kSf = kSfF + 2 * 512 * kTokBlocks;  // scales of a stage
-  static constexpr int kStages = 5, kUnits = 8;
+  static constexpr int kStages = TN > 128 ? 5 : 7, kUnits = 8;
   static constexpr int kOut = 2 * kChunk * kTF * 2;                // two staging buffers, bf16
   static constexpr int kBars = 512;
   static constexpr int kSmem = kStages * kCodes + kUnits * 2 * kSf + kOut + kBars + 1024;
@@ -458,13 +459,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
 // ------------------------------------------------------------- few tokens
 //
-// Up to 64 tokens the product is a stream of the weights.  A cluster of C blocks
-// shares a tile of 128 features: block r takes the r-th part of K, and the
-// partial sums meet through distributed shared memory, added in rank order (no
-// workspace, no atomics, the same bits every time).  C grows while the blocks
-// stay at about one per SM and each has two stages: a second wave costs more
-// than the split gains (us, one token, K = 5,120, C = 1 / 2 / 4 / 8: N = 5,120
-// 11.3 / 8.7 / 8.7 / 12.2; N = 15,360 12.2 / 12.6 / 16.6 / 25.5).
+// Up to 64 tokens (and somewhat beyond, with few features and a long K) the
+// product is a stream of the weights.  A cluster of C blocks shares a tile of 128
+// features: block r takes the r-th part of K, and the partial sums meet through
+// distributed shared memory, added in rank order (no workspace, no atomics, the
+// same bits every time).  C grows while the blocks stay at about one per SM and
+// each has two stages: a second wave costs more than the split gains (us, one
+// token, K = 5,120, C = 1 / 2 / 4 / 8: N = 5,120 11.3 / 8.7 / 8.7 / 12.2; N =
+// 15,360 12.2 / 12.6 / 16.6 / 25.5).
 
 constexpr int kFewThreads = 256;  // warp 0 TMA, 1 MMA, 4-7 scales, then the sums
 
@@ -692,6 +694,14 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   }
 }
 
+// Blocks that share a tile of 128 features x TN tokens in k_mx_few.
+int few_split(int tiles, int kblocks) {
+  int C = 1;
+  while (C < 8 && tiles * C * 2 <= 160 && kblocks >= 4 * C) C *= 2;
+  return C;
+}
+int few_tiles(int M, int N, int TN) { return (int)std::min(1LL << 30, (long long)((N + kTF - 1) / kTF) * ((M + TN - 1) / TN)); }
+
 template <int TN>
 cudaError_t launch_few(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_codes, cudaStream_t st) {
   using T = FewTile<TN>;
@@ -701,9 +711,8 @@ cudaError_t launch_few(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_c
   const cudaError_t e = cudaFuncSetAttribute(k_mx_few<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
   if (e != cudaSuccess) return e;
   p.ftiles = (p.N + kTF - 1) / kTF;
-  p.tiles = p.ftiles * ((p.M + TN - 1) / TN);
-  int C = 1;
-  while (C < 8 && p.tiles * C * 2 <= 160 && p.kblocks >= 4 * C) C *= 2;
+  p.tiles = few_tiles(p.M, p.N, TN);
+  const int C = few_split(p.tiles, p.kblocks);
   note_launch();
   return launch_chained(k_mx_few<TN>, p.tiles * C, kFewThreads, T::kSmem, C, st, map_w, map_a, p, C);
 }
@@ -722,10 +731,13 @@ cudaError_t launch_pair(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_
   return launch_chained(k_mx_pair<TN>, 2 * std::min(p.tiles, 74), kPairThreads, T::kSmem, 0, st, map_w, map_a, p);
 }
 
-// Rounds of tiles that 74 pairs of SMs take.
-long long pair_rounds(int M, int N, int TN) {
+// Relative time of a product in tiles of TN tokens: the rounds of tiles that 74
+// pairs of SMs take, times what a round takes (2,048 x 15,360 x 5,120, us for a
+// round of 64 / 128 / 192: 6.0 / 7.5 / 8.7; one of 224 takes 1.04 to 1.13 times
+// one of 192, since its scales wait).
+long long pair_cost(int M, int N, int TN) {
   const long long tiles = (long long)((N + 2 * kTF - 1) / (2 * kTF)) * ((M + TN - 1) / TN);
-  return (tiles + 73) / 74;
+  return (tiles + 73) / 74 * (TN + (TN > 192 ? 256 : 237));
 }
 
 }  // namespace
@@ -740,15 +752,23 @@ cudaError_t mx_product_run(const uint8_t* a_codes, const uint8_t* a_scales, cons
   p.status = status_word();
   if (!p.status) return cudaErrorInvalidValue;
   if (M <= 16) return launch_few<16>(p, a_codes, w_codes, st);
-  // From 65 tokens on the wide tiles win even where they leave SMs idle.
-  if (M <= 64) return launch_few<64>(p, a_codes, w_codes, st);
-  // A round of 224 tokens takes 1.05 to 1.12 times a round of 192 (1,000 x 5,120 x
-  // 5,120: 24.0 against 21.7 us for two rounds), so it has to save 3 rounds in 23:
-  // 16,384 x 2,048 x 2,048 takes 42 us in 8 rounds of 224 and 50 in 10 of 192,
-  // 200 x 15,360 x 5,120 17.4 in one and 21.3 in two, 75,600 x 15,360 x 5,120 2.53
-  // ms and 2.72; 6,000 x 5,120 x 5,120, 8 rounds against 9, takes 75 and 74 us.
-  return 20 * pair_rounds(M, N, 192) > 23 * pair_rounds(M, N, 224) ? launch_pair<224>(p, a_codes, w_codes, st)
-                                                                   : launch_pair<192>(p, a_codes, w_codes, st);
+  // Beyond 64 tokens a long K that four blocks or more would share is still theirs
+  // (us, this / pairs: 128 x 2,048 x 8,192 9.6 / 15.3; 512 x 512 x 8,192 9.6 /
+  // 13.8; with two blocks 300 x 2,048 x 8,192 15.5 / 15.3, with one 512 x 2,048 x
+  // 8,192 17.8 / 15.5).
+  if (M <= 64 || few_split(few_tiles(M, N, 64), p.kblocks) >= 4) return launch_few<64>(p, a_codes, w_codes, st);
+  // The width whose rounds take the least (us for 64 / 128 / 192 / 224 tokens:
+  // 512 x 2,048 x 2,048 7.9 / 8.4 / 9.3 / 10.1; 2,048 x 2,048 x 2,048 14.7 / 11.1
+  // / 12.0 / 11.9; 512 x 5,120 x 5,120 22.8 / 18.5 / 14.7 / 16.0; 1,500 x 5,120 x
+  // 5,120 45.4 / 30.7 / 27.7 / 24.3; 75,600 x 15,360 x 5,120 at 192 / 224 2,720 /
+  // 2,530).
+  int best = 64;
+  for (const int tn : {128, 192, 224})
+    if (pair_cost(M, N, tn) <= pair_cost(M, N, best)) best = tn;
+  if (best == 64) return launch_pair<64>(p, a_codes, w_codes, st);
+  if (best == 128) return launch_pair<128>(p, a_codes, w_codes, st);
+  if (best == 192) return launch_pair<192>(p, a_codes, w_codes, st);
+  return launch_pair<224>(p, a_codes, w_codes, st);
 }
 
 }  // namespace svg

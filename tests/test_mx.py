@@ -144,7 +144,7 @@ def product_check(a, sa, w, sw, bias, got):
     (1, 8, 32, False), (16, 128, 64, False), (16, 128, 256, False), (16, 128, 512, True), (5, 136, 160, True),
     (17, 120, 288, False), (64, 256, 1024, True), (65, 128, 96, True), (192, 128, 256, False), (193, 1000, 2080, True),
     (500, 264, 352, True), (1, 30720, 512, True), (33, 2048, 5120, False), (1000, 5120, 2048, True), (3000, 1032, 4128, True),
-    (14337, 2304, 544, True), (224, 256, 1312, False),
+    (14337, 2304, 544, True), (224, 256, 1312, False), (200, 264, 8224, True), (900, 2056, 416, False), (512, 512, 8192, True),
     (2, 40, 16384, False)])
 def test_product(M, N, K, bias):
     a, sa = weights(M, K, 1)

@@ -812,7 +812,8 @@ struct Shape {
   long long workers;
 };
 
-constexpr int kSmemPerSm = 228 * 1024, kSmemPerBlock = 2048;  // 1 KB per block is the system's, the rest static arrays
+// Per block 1 KB is the system's, 1.25 KB are static arrays.
+constexpr int kSmemPerSm = 228 * 1024, kSmemPerBlock = 2304;
 // What the rings of an SM's blocks hold together.  Beyond about 80 KB more reads
 // in flight only delay the writes (share of the copy rate: bf16 65,536 x 2,048
 // with 64 / 96 / 195 KB 0.94 / 0.84 / 0.80; float32 40,000 x 2,048 with 64 / 96

@@ -334,6 +334,40 @@ def test_more_than_2_to_the_31_elements():
 
 # ------------------------------------------------------------------ refusals
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("types", [(BF, BF), (F32, F32), (F32, BF)])
+def test_every_width(types):
+    """Every number of columns, three rows and more per worker, against 64 bits on the device.  A sum of squares and
+    the products of an RMS norm lose no digits, so K u of each term's magnitude bounds what precedes the rounding."""
+    N, g = 450, torch.Generator(device="cuda").manual_seed(5)
+    half = {BF: 2.0 ** -8, F32: 2.0 ** -24}
+    wide = [torch.randn(N, 8192, generator=g, device="cuda") for _ in range(4)]
+    mods = [torch.randn(1, 8192, generator=g, device="cuda") * 0.5 for _ in range(3)]
+    for D in range(8, 8193, 8):
+        x, y, dr, dh = (t[:, :D].to(k).contiguous() for t, k in zip(wide, (types[0], types[1]) * 2))
+        gate, scale, shift = (t[:, :D].contiguous() for t in mods)
+        kw = dict(gate=gate, scale=scale, pre=sv.SVGEAR_NORM_RMS)
+        r, h = sv.block_norm(x, y, shift=shift, **kw)
+        back = sv.block_norm_backward(x, y, dr, dh, shift=shift, **kw)
+        X, Y, DR, DH, A, S, T = (t.double() for t in (x, y, dr, dh, gate, scale, shift))
+        R = X + A * Y
+        inv = 1 / torch.sqrt((R * R).mean(1, keepdim=True) + 1e-6)
+        n, u = R * inv, DH * (1 + S)
+        size = (X.abs() + (A * Y).abs()) * inv  # of the normed row before a and g y may cancel
+        dR = DR + inv * (u - n * (u * n).mean(1, keepdim=True))
+        mag = DR.abs() + inv * (u.abs() + size * (u * size).abs().mean(1, keepdim=True))
+        for name, got, ref, m, k in (("r", r, R, X.abs() + (A * Y).abs(), types[0]),
+                                     ("h", h, n * (1 + S) + T, size * (1 + S.abs()) + T.abs(), types[1]),
+                                     ("dx", back["dx"], dR, mag, types[0]),
+                                     ("dy", back["dy"], dR * A, mag * A.abs(), types[1])):
+            over = (got.double() - ref).abs() - (half[k] * ref.abs() + K * U * m)
+            assert over.max() <= 0, (name, D, over.max().item())
+        for name, ref in (("dscale", DH * n), ("dgate", dR * Y)):
+            m = DH.abs() * size if name == "dscale" else mag * Y.abs()
+            over = (back[name].double() - ref.sum(0)).abs() - (K + N) * U * m.sum(0)
+            assert over.max() <= 0, (name, D, over.max().item())
+
+
 @pytest.fixture(scope="module")
 def L():
     build()

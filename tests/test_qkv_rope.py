@@ -295,6 +295,38 @@ def test_nan_and_zero_tokens_stay_in_their_rows():
 
 # ------------------------------------------------------------------ refusals
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("norm", ["none", "head", "token"])
+def test_every_head_count(d, dtype, norm):
+    """Every number of heads, there and back.  Without a norm the way back restores the rows: each way is within
+    eps/2 + K u of a pair's magnitude."""
+    N, g = 450, torch.Generator(device="cuda").manual_seed(6)
+    axes, grid = ((16, 24, 24) if d == 64 else (44, 42, 42)), (2, 15, 15)
+    wide = torch.randn(N, 16384 // d, d, generator=g, device="cuda").to(dtype)
+    w = 1 + 0.3 * torch.randn(16384, generator=g, device="cuda")
+    for H in range(1, 16384 // d + 1):
+        x = wide[:, :H].contiguous()
+        cols = {"none": None, "head": d, "token": H * d}[norm]
+        kw = dict(axes=axes, grid=grid, norm=NORM[norm], wq=None if cols is None else w[:cols].contiguous())
+        Q, Km, V = sv.qkv_rope(x, x, x, **kw)
+        assert torch.equal(V, x.transpose(0, 1)), H
+        back = sv.qkv_rope_backward(Q, Km, V, x, x, **kw)
+        assert torch.equal(back["dv"], x), H
+        if norm == "none":
+            lim = 2 * (HALF[dtype] + K * U) * 2 * x.double().abs().amax()
+            assert (back["dq"].double() - x.double()).abs().max() <= lim and torch.equal(back["dq"], back["dk"]), H
+        else:
+            X = x.double()
+            inv = 1 / torch.sqrt((X * X).mean((-1,) if norm == "head" else (-2, -1), keepdim=True) + 1e-6)
+            W = (w[:cols].view(1, 1, d) if norm == "head" else w[:cols].view(1, H, d)).double()
+            size = (Q.double() ** 2).sum(-1)  # a rotation keeps a head's length
+            ref = ((X * inv * W) ** 2).sum(-1).T
+            assert ((size - ref).abs() <= (2 * HALF[dtype] * 1.01 + 2 * K * U) * 2 * ref).all(), H
+            assert back["dq"].isfinite().all() and back["dwq"].isfinite().all() and back["dwk"] is None, H
+
+
 @pytest.fixture(scope="module")
 def L():
     build()

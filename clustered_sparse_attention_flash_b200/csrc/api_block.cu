@@ -14,7 +14,12 @@ inline bool aligned16(const P*... p) {
   return ((reinterpret_cast<uintptr_t>(p) | ...) & 15u) == 0;
 }
 inline cudaStream_t S(void* s) { return static_cast<cudaStream_t>(s); }
-inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? SVGEAR_OK : SVGEAR_ERR_CUDA; }
+// A refused launch is reported here and does not stay behind as the thread's last error.
+inline int cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return SVGEAR_OK;
+  cudaGetLastError();
+  return SVGEAR_ERR_CUDA;
+}
 inline bool known_dtype(int t) { return t == SVGEAR_F32 || t == SVGEAR_BF16; }
 inline int esize(int dtype) { return dtype == SVGEAR_BF16 ? 2 : 4; }
 

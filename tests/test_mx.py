@@ -254,6 +254,25 @@ def test_linears_in_a_row(M):
         assert torch.equal(y, want)
 
 
+@pytest.mark.gpu
+def test_linears_on_two_streams_at_once():
+    """Narrow, split and wide products beside each other: the bits of each alone."""
+    shapes = [(1, 4096, 1024), (40, 512, 4096), (300, 1024, 2048), (2000, 2048, 512)]
+    calls = []
+    for i, (M, N, K) in enumerate(shapes):
+        x = torch.randn(M, K, generator=torch.Generator().manual_seed(i)).cuda().bfloat16()
+        w = tuple(t.cuda() for t in weights(N, K, i))
+        calls.append((x, w, sv.mx_linear(x, *w)))
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for i in range(40):
+        x, w, want = calls[(i // 2 + (i & 1) * (1 + i // 8)) % 4]
+        got.append((sv.mx_linear(x, *w, stream=streams[i & 1]), want))
+    torch.cuda.synchronize()
+    assert sv.svgear_get_status() == sv.SVGEAR_OK
+    assert all(torch.equal(y, want) for y, want in got)
+
+
 # ------------------------------------------------------------------ refusals
 
 @pytest.fixture(scope="module")

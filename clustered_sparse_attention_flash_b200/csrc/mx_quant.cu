@@ -62,22 +62,46 @@ __device__ __forceinline__ float e8m0(uint32_t b) {
 constexpr int kThreads = 256;
 constexpr int kBatch = 4;  // vectors of a thread in flight
 
+// The largest magnitude of a vector, as the bits of a float (a NaN is above all).
+__device__ __forceinline__ uint32_t top_bits(const Raw<float>& r) {
+  const uint32_t m = 0x7fffffffu;
+  const uint32_t a = max(__float_as_uint(r.a.x) & m, __float_as_uint(r.a.y) & m), b = max(__float_as_uint(r.a.z) & m, __float_as_uint(r.a.w) & m);
+  const uint32_t c = max(__float_as_uint(r.b.x) & m, __float_as_uint(r.b.y) & m), d = max(__float_as_uint(r.b.z) & m, __float_as_uint(r.b.w) & m);
+  return max(max(a, b), max(c, d));
+}
+__device__ __forceinline__ uint32_t top_bits(const Raw<bf16>& r) {
+  auto mag = [](uint32_t w) {
+    w &= 0x7fff7fffu;
+    return *reinterpret_cast<const __nv_bfloat162*>(&w);
+  };
+  const __nv_bfloat162 t = __hmax2_nan(__hmax2_nan(mag(r.u.x), mag(r.u.y)), __hmax2_nan(mag(r.u.z), mag(r.u.w)));
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&t);
+  return max(w << 16, w & 0xffff0000u);
+}
+
 // One vector of a block of 32: its codes and the scale byte, which the block's
 // four lanes agree on.
-__device__ __forceinline__ uint32_t quantise(float (&f)[kVec], uint32_t& byte) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+template <typename T>
+__device__ __forceinline__ uint32_t quantise(const Raw<T>& r, uint32_t& byte) {
+  uint32_t top = top_bits(r);
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   const uint32_t e = top >> 23;  // biased exponent of the largest magnitude
   const bool bad = e == 255u;
   byte = bad ? 255u : e > 2u ? e - 2u : 0u;
   // 1 / scale = 2^(127 - byte): a normal float for every byte up to 252
-  const float inv = bad ? 0.f : __uint_as_float((254u - byte) << 23);
+  const f2 inv = pair(__uint_as_float((254u - byte) << 23));
+  Vec v;
+  unpack(r, v);
+  float f[kVec];
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) f[i] = bad ? 0.f : f[i] * inv;
-  return pack_e2m1(f);
+  for (int i = 0; i < 4; ++i) {
+    const float2 h = halves(mul2(v.v[i], inv));
+    f[2 * i] = h.x;
+    f[2 * i + 1] = h.y;
+  }
+  const uint32_t c = pack_e2m1(f);
+  return bad ? 0u : c;
 }
 
 // X is [M][K] (head_d = 0) or head-major [K/head_d][M][head_d]; four threads
@@ -105,10 +129,8 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize(const T* __restrict__ 
   }
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
-    float f[kVec];
-    unpack(r[u], f);
     uint32_t byte;
-    const uint32_t c = quantise(f, byte), i = u * kThreads + threadIdx.x;
+    const uint32_t c = quantise(r[u], byte), i = u * kThreads + threadIdx.x;
     if (i < left) {
       codes[base + i] = c;
       if ((threadIdx.x & 3) == 0) scales[(base + i) >> 2] = (uint8_t)byte;
@@ -134,10 +156,8 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize_heads(const T* __restr
   }
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
-    float f[kVec];
-    unpack(r[u], f);
     uint32_t byte;
-    const uint32_t c = quantise(f, byte);
+    const uint32_t c = quantise(r[u], byte);
     if (row < M && h0 + u < H) {
       const long long i = (row * H + h0 + u) * vph + vec;
       codes[i] = c;

@@ -9,8 +9,10 @@
 // shows in everything computed from it.
 //
 // HBM-bound: x in, half a byte plus 1/32 byte per element out.  Measured on a
-// B200, 32,768 x 2,048 bf16: quantisation 30.4 us, 5.6 TB/s (0.85 of a plain
-// copy), dequantisation 27.8 us, 6.1 TB/s (0.93).
+// B200, 32,768 x 2,048 bf16: quantisation of rows 26.1 us, 6.5 TB/s (0.99 of a plain
+// copy), of head-major rows 27.0 us (0.96; 75,600 x 5,120 166 us, 0.90),
+// dequantisation 27.8 us (0.93).  With the maximum taken element by element in
+// float32 the issue slots bound it: 31.5 and 30.5 us.
 #include <cuda_fp16.h>
 
 #include "chain.cuh"
@@ -140,7 +142,9 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize(const T* __restrict__ 
 
 // Head-major X whose heads are 2^n vectors wide: a block takes kThreads / 2^n
 // tokens of kBatch neighbouring heads, so that it reads whole kilobytes (32,768
-// tokens of 16 heads of 128: 43.9 us in the order of the rows, 30.4 us in this).
+// tokens of 16 heads of 128, before the packed maximum: 43.9 us in the order of
+// the rows, 30.4 us in this; now 29.2 us with the head groups of a run of tokens
+// in neighbouring blocks, 27.0 us in this order).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_mx_quantize_heads(const T* __restrict__ X, int M, int H, int log_vph,
                                                                 uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {

@@ -5,8 +5,8 @@
 // calls launch_next() lets such a successor begin once all its own blocks have
 // begun.  Any other successor waits for its end as ever.
 //
-// The quantisation calls launch_next() and the product is launched chained: 1.0
-// to 1.6 us less for the two (us, tokens x features x K, before / after: 1 x
+// The quantisation calls launch_next(); the product and the dequantisation are
+// launched chained: 1.0 to 1.6 us less for quantisation and product (us, tokens x features x K, before / after: 1 x
 // 2,048 x 2,048 6.9 / 5.9; 1 x 30,720 x 5,120 19.8 / 18.9; 128 x 5,120 x 5,120
 // 17.0 / 15.5).  Kernels that fill every SM for long lose by it, since their
 // early blocks spread unevenly (the product of 64 tokens after itself 15.0 / 19.2

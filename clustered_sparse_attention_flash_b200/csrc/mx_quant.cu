@@ -171,9 +171,8 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize_heads(const T* __restr
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_mx_dequantize(const uint32_t* __restrict__ codes,
-                                                            const uint8_t* __restrict__ scales, long long vecs,
-                                                            T* __restrict__ Y) {
+__global__ void __launch_bounds__(kThreads) k_mx_dequantize(const uint32_t* codes, const uint8_t* scales, long long vecs, T* Y) {
+  wait_previous(codes, scales, Y);
   const long long base = (long long)blockIdx.x * (kThreads * kBatch) + threadIdx.x;
   uint32_t c[kBatch], e[kBatch];
 #pragma unroll
@@ -228,10 +227,9 @@ cudaError_t mx_dequantize_run(const uint8_t* codes, const uint8_t* scales, int M
   const long long vecs = (long long)M * (K / kVec);
   const int grid = (int)((vecs + kThreads * kBatch - 1) / (kThreads * kBatch));
   const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
-  if (dtype == DT_F32) k_mx_dequantize<float><<<grid, kThreads, 0, st>>>(c, scales, vecs, static_cast<float*>(Y));
-  else k_mx_dequantize<bf16><<<grid, kThreads, 0, st>>>(c, scales, vecs, static_cast<bf16*>(Y));
   note_launch();
-  return cudaGetLastError();
+  if (dtype == DT_F32) return launch_chained(k_mx_dequantize<float>, grid, kThreads, 0, 0, st, c, scales, vecs, static_cast<float*>(Y));
+  return launch_chained(k_mx_dequantize<bf16>, grid, kThreads, 0, 0, st, c, scales, vecs, static_cast<bf16*>(Y));
 }
 
 }  // namespace svg

@@ -6,11 +6,12 @@
 // begun.  Any other successor waits for its end as ever.
 //
 // The quantisation calls launch_next(); the product and the dequantisation are
-// launched chained: 1.0 to 1.6 us less for quantisation and product (us, tokens x features x K, before / after: 1 x
-// 2,048 x 2,048 6.9 / 5.9; 1 x 30,720 x 5,120 19.8 / 18.9; 128 x 5,120 x 5,120
-// 17.0 / 15.5).  Kernels that fill every SM for long lose by it, since their
-// early blocks spread unevenly (the product of 64 tokens after itself 15.0 / 19.2
-// us, a norm of 2,500 rows after itself 34.6 / 38.9): they do not call it.
+// launched chained: 1.0 to 1.6 us less for quantisation and product (us, tokens x
+// features x K, before / after: 1 x 2,048 x 2,048 6.9 / 5.9; 1 x 30,720 x 5,120
+// 19.8 / 18.9; 128 x 5,120 x 5,120 17.0 / 15.5).  Kernels that fill every SM for
+// long lose by it, since their early blocks spread unevenly (the product of 64
+// tokens with 15,360 features after itself 15.0 / 19.2 us, a norm of 4,999 rows
+// after itself 34.6 / 38.9): they do not call it.
 #pragma once
 #include <cuda_runtime.h>
 

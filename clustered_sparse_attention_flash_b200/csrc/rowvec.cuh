@@ -25,18 +25,6 @@ __device__ __forceinline__ void load_raw(Raw<float>& v, const float* p) {
 }
 __device__ __forceinline__ void zero_raw(Raw<bf16>& v) { v.u = make_uint4(0, 0, 0, 0); }
 __device__ __forceinline__ void zero_raw(Raw<float>& v) { v.a = v.b = make_float4(0.f, 0.f, 0.f, 0.f); }
-__device__ __forceinline__ void unpack(const Raw<bf16>& v, float (&f)[kVec]) {
-  const uint32_t w[4] = {v.u.x, v.u.y, v.u.z, v.u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void unpack(const Raw<float>& v, float (&f)[kVec]) {
-  f[0] = v.a.x; f[1] = v.a.y; f[2] = v.a.z; f[3] = v.a.w;
-  f[4] = v.b.x; f[5] = v.b.y; f[6] = v.b.z; f[7] = v.b.w;
-}
 __device__ __forceinline__ void store_raw(bf16* p, const Raw<bf16>& v) { *reinterpret_cast<uint4*>(p) = v.u; }
 __device__ __forceinline__ void store_raw(float* p, const Raw<float>& v) {
   reinterpret_cast<float4*>(p)[0] = v.a;
@@ -56,12 +44,6 @@ __device__ __forceinline__ void store_vec(float* p, const float (&f)[kVec]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
-__device__ __forceinline__ void load_f8(float (&f)[kVec], const float* p) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-
 // Two floats in one register pair: the packed float32 instructions of sm_100
 // do twice the work per issue slot.
 typedef unsigned long long f2;

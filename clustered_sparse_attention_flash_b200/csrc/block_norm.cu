@@ -885,7 +885,7 @@ template <typename TX, typename TY, int CLS>
 cudaError_t launch_class(const NormArgs& p, const Shape& s, bool back, cudaStream_t st) {
   const auto kernel = back ? k_block_norm_back<TX, TY, CLS> : k_block_norm<TX, TY, CLS>;
   if (s.smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem);
+    const cudaError_t e = allow_dynamic_smem(kernel, kSmemPerSm - kSmemPerBlock);
     if (e != cudaSuccess) return e;
   }
   kernel<<<s.grid, s.block, s.smem, st>>>(p);

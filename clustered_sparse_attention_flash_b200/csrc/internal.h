@@ -117,6 +117,15 @@ bool tma_map_bf16_3d(void* map, const void* base, uint64_t d0, uint64_t d1, uint
 // and 128-byte swizzle; what lies outside reads as zeros.
 bool tma_map_u8_rows(void* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);
 
+// Lets `kernel` be launched with up to `most` bytes of dynamic shared memory.  The
+// limit belongs to the function and not to a launch, and other host threads may
+// launch the same function at this moment: `most` is a constant of the kernel,
+// the most that any call of it asks for, so that no call lowers it under another.
+template <typename K>
+inline cudaError_t allow_dynamic_smem(K* kernel, int most) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Bump allocator over a caller-provided workspace.

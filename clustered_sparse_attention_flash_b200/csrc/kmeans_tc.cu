@@ -789,7 +789,7 @@ static cudaError_t assign_launch(const bf16* X, int H, int N, int C, const float
     const int stages = pick_stages(D, sr, sp);
     const int pmode = (c_base > 0 ? 1 : 0) | (c_base + seg < Cpad ? 2 : 0);
     const int smem = layout(D, sr, sp, stages).total;
-    cudaError_t e = cudaFuncSetAttribute(k_assign_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_dynamic_smem(k_assign_tc<D>, kSmemLimit);
     if (e != cudaSuccess) return e;
     k_assign_tc<D><<<dim3((T + tpc - 1) / tpc, H), kThreads, smem, st>>>(
         tmx, tmc, w.table, w.bd, w.xn, N, sp, sr, stages, tpc, nbits, labels, w.list2, w.list_full,

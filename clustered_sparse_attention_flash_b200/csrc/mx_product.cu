@@ -708,7 +708,7 @@ cudaError_t launch_few(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_c
   CUtensorMap map_w, map_a;
   if (!tma_map_u8_rows(&map_w, w_codes, p.K / 2, p.N, kTF) || !tma_map_u8_rows(&map_a, a_codes, p.K / 2, p.M, TN))
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(k_mx_few<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+  const cudaError_t e = allow_dynamic_smem(k_mx_few<TN>, T::kSmem);
   if (e != cudaSuccess) return e;
   p.ftiles = (p.N + kTF - 1) / kTF;
   p.tiles = few_tiles(p.M, p.N, TN);
@@ -723,7 +723,7 @@ cudaError_t launch_pair(ProductArgs p, const uint8_t* a_codes, const uint8_t* w_
   CUtensorMap map_w, map_a;
   if (!tma_map_u8_rows(&map_w, w_codes, p.K / 2, p.N, kTF) || !tma_map_u8_rows(&map_a, a_codes, p.K / 2, p.M, TN / 2))
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(k_mx_pair<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+  const cudaError_t e = allow_dynamic_smem(k_mx_pair<TN>, T::kSmem);
   if (e != cudaSuccess) return e;
   p.ftiles = (p.N + 2 * kTF - 1) / (2 * kTF);
   p.tiles = p.ftiles * ((p.M + TN - 1) / TN);

@@ -836,7 +836,7 @@ template <typename T, bool HALF, int CLS, int D>
 cudaError_t launch_class(const RopeArgs& a, const Shape& s, bool back, cudaStream_t st) {
   const auto kernel = back ? k_qkv_rope_back<T, HALF, CLS, D> : k_qkv_rope<T, HALF, CLS, D>;
   if (s.smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem);
+    const cudaError_t e = allow_dynamic_smem(kernel, kSmemPerSm - kSmemPerBlock);
     if (e != cudaSuccess) return e;
   }
   kernel<<<s.grid, s.block, s.smem, st>>>(a);

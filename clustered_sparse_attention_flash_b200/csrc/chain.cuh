@@ -1,9 +1,11 @@
 // Launching a kernel before the one ahead of it in the stream has ended
 // (programmatic dependent launch), so that its launch and prologue hide behind
 // that kernel's tail.  A kernel launched by launch_chained calls wait_previous()
-// before it touches memory that another kernel may write or read; a kernel that
-// calls launch_next() lets such a successor begin once all its own blocks have
-// begun.  Any other successor waits for its end as ever.
+// before it touches memory that another kernel may write or read, and reads such
+// memory with coherent loads only: a non-coherent one (__ldg, __restrict__) is for
+// memory that nothing writes while the kernel lives.  A kernel that calls
+// launch_next() lets such a successor begin once all its own blocks have begun.
+// Any other successor waits for its end as ever.
 //
 // The quantisation calls launch_next(); the product and the dequantisation are
 // launched chained: 1.0 to 1.6 us less for quantisation and product (us, tokens x

@@ -65,20 +65,21 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
 }
 
 // Scales [16 u, 16 u + 16) of a row with `pitch` scales (two stages); 0 behind
-// the end.  As wide as the rows are aligned.
+// the end.  As wide as the rows are aligned, and coherent loads: the kernel ahead
+// may write the scales while this one is already running (chain.cuh).
 __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pitch, int u) {
   const uint8_t* s = row + u * 16;
-  if ((pitch & 15) == 0) return __ldg(reinterpret_cast<const uint4*>(s));
+  if ((pitch & 15) == 0) return *reinterpret_cast<const uint4*>(s);
   uint32_t v[4] = {0, 0, 0, 0};
   const int left = pitch - u * 16;
   if ((pitch & 3) == 0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (4 * i < left) v[i] = __ldg(reinterpret_cast<const uint32_t*>(s) + i);
+      if (4 * i < left) v[i] = reinterpret_cast<const uint32_t*>(s)[i];
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (i < left) v[i >> 2] |= (uint32_t)__ldg(s + i) << (8 * (i & 3));
+      if (i < left) v[i >> 2] |= (uint32_t)s[i] << (8 * (i & 3));
   }
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
@@ -485,16 +486,16 @@ struct FewTile {
 // Scales [8 kb, 8 kb + 8) of a row with `pitch` scales (one stage); 0 behind the end.
 __device__ __forceinline__ uint2 load_scales8(const uint8_t* row, int pitch, int kb) {
   const uint8_t* s = row + kb * 8;
-  if ((pitch & 7) == 0) return __ldg(reinterpret_cast<const uint2*>(s));
+  if ((pitch & 7) == 0) return *reinterpret_cast<const uint2*>(s);
   const int left = pitch - kb * 8;
   uint32_t v[2] = {0, 0};
   if ((pitch & 3) == 0) {
-    v[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
-    if (left > 4) v[1] = __ldg(reinterpret_cast<const uint32_t*>(s) + 1);
+    v[0] = *reinterpret_cast<const uint32_t*>(s);
+    if (left > 4) v[1] = reinterpret_cast<const uint32_t*>(s)[1];
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < left) v[i >> 2] |= (uint32_t)__ldg(s + i) << (8 * (i & 3));
+      if (i < left) v[i >> 2] |= (uint32_t)s[i] << (8 * (i & 3));
   }
   return make_uint2(v[0], v[1]);
 }

@@ -275,6 +275,23 @@ def test_linears_on_two_streams_at_once():
 
 # ------------------------------------------------------------------ refusals
 
+def test_chained_kernels_load_coherently():
+    """A kernel that may run beside the one ahead of it must not promise that what it reads is constant."""
+    import pathlib
+    import re
+    src = pathlib.Path(sv.HERE) / "csrc"
+    chained = 0
+    for f in sorted(src.glob("*.cu")):
+        code = re.sub(r"//[^\n]*", "", f.read_text())
+        # a kernel and what it calls in its file: the product's file whole, the dequantisation's own text
+        parts = [code] if f.name == "mx_product.cu" else re.split(r"(?=\n(?:template|__global__))", code)
+        for part in parts:
+            if "wait_previous(" in part:
+                chained += 1
+                assert not re.search(r"__ldg|__restrict__|\.nc\b", part), (f.name, part[:200])
+    assert chained == 2
+
+
 @pytest.fixture(scope="module")
 def L():
     build()

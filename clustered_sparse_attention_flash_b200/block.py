@@ -38,7 +38,9 @@ def attention_block(x, w: BlockWeights, H: int, *, Cq: int, Ck: int, iters: int,
                     offsets=None, init_q=None, init_k=None, ws=None, eps: float = 1e-6):
     """x [N, D] (bfloat16, or float32 with the branch in bfloat16) is the residual stream of one sample;
     shift, scale, gate and next_* are float32 [G, D] modulations over the groups of `offsets` (or N/G rows
-    each).  ws is a workspace of svgear_workspace_size bytes to keep between calls.  Returns (r, h): the new
+    each).  The attention is over all N rows: rows from offsets[G] on belong to no group, enter the projection
+    as zeros and are zero in r and h, so a sample's padding is left out of x, not behind the last group.
+    ws is a workspace of svgear_workspace_size bytes to keep between calls.  Returns (r, h): the new
     residual stream and the normed, modulated input of the block's other half."""
     import torch
     with torch.cuda.device(x.device):

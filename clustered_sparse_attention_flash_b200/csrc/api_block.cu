@@ -29,7 +29,8 @@ constexpr int kMaxRows = 1 << 30;  // row counters are int, and run ahead by a f
 
 int check_norm(const svgear_norm_params* p) {
   if (!p || p->N < 1 || p->D < 1 || p->G < 1) return SVGEAR_ERR_INVALID;
-  if (p->pre < SVGEAR_NORM_NONE || p->pre > SVGEAR_NORM_LAYER) return SVGEAR_ERR_INVALID;
+  const int pre = p->pre & ~SVGEAR_NORM_CLEAR_REST;
+  if (pre < SVGEAR_NORM_NONE || pre > SVGEAR_NORM_LAYER) return SVGEAR_ERR_INVALID;
   if (p->post < SVGEAR_NORM_NONE || p->post > SVGEAR_NORM_LAYER) return SVGEAR_ERR_INVALID;
   if (!(p->eps > 0.f) || std::isinf(p->eps) || !std::isfinite(p->res_scale)) return SVGEAR_ERR_INVALID;
   if (!known_dtype(p->dtype) || !known_dtype(p->res_dtype)) return SVGEAR_ERR_UNSUPPORTED;

@@ -41,7 +41,7 @@ struct NormArgs {
   const void *x, *y, *dr, *dh;
   const float *gate, *scale, *shift, *weight, *bias, *post_weight;
   const int32_t* offsets;
-  int N, D, G, pre, post, tpr, chunk, stages, ring_bytes;
+  int N, D, G, pre, post, clear, tpr, chunk, stages, ring_bytes;
   float eps, a;
   void *r, *h, *dx, *dy;
   float* part;  // backward: [slots][3][D] partial column sums
@@ -332,6 +332,21 @@ __device__ __forceinline__ Place place(const NormArgs& p) {
   return q;
 }
 
+// The rows of a worker's run behind the last group, which belong to none: zeros,
+// or those of `from`.  A run's rows lie side by side.
+template <bool NARROW, typename T>
+__device__ __forceinline__ void clear_rest(const NormArgs& p, const Place& q, void* to, const void* from = nullptr) {
+  if (!to) return;
+  const int threads = NARROW ? 32 : blockDim.x, t = NARROW ? threadIdx.x & 31 : threadIdx.x;
+  const long long till = min((long long)q.row + p.chunk, (long long)p.N) * p.D;
+  for (long long i = (long long)max(q.row, q.end) * p.D + t * kVec; i < till; i += threads * kVec) {
+    Raw<T> v;
+    zero_raw(v);
+    if (from) load_raw(v, static_cast<const T*>(from) + i);
+    store_raw(static_cast<T*>(to) + i, v);
+  }
+}
+
 // Steps through a run: `base` the first row of this step, `next` of the one
 // behind it, `g` the rows' group, which ends (for this run) at `stop`.
 struct Walk {
@@ -460,6 +475,10 @@ __global__ void __launch_bounds__(Class<CLS, false>::kMax, (Class<CLS, false>::k
   Columns<V> c;
   c.init(p.D, p.tpr, pl.lane, sum);
   typename std::conditional<CLS == 0, Direct<TX, TY, 2, V>, Ring<TX, TY, 2, V>>::type rows(p, c, pl.row + pl.sub, pl.end);
+  if (p.clear && pl.end < pl.row + p.chunk) {
+    clear_rest<CLS == 0, TX>(p, pl, p.r);
+    clear_rest<CLS == 0, TY>(p, pl, p.h);
+  }
   Walk at(p, pl);
   // a sum over the block is the barrier behind which a stage is free
   const bool barrier = (p.y && p.post != SVGEAR_NORM_NONE) || (p.h && p.pre != SVGEAR_NORM_NONE);
@@ -584,6 +603,10 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
   Columns<V> c;
   c.init(p.D, p.tpr, pl.lane, sum);
   typename std::conditional<CLS == 0, Direct<TX, TY, 4, V>, Ring<TX, TY, 4, V>>::type rows(p, c, pl.row + pl.sub, pl.end);
+  if (p.clear && pl.end < pl.row + p.chunk) {
+    clear_rest<CLS == 0, TX>(p, pl, p.dx, p.y ? nullptr : p.dr);  // without y, r is x there too
+    clear_rest<CLS == 0, TY>(p, pl, p.dy);
+  }
   Walk at(p, pl);
   // Rows are read to the end of their iteration.  With four stages or more the
   // barrier in the next row's sum frees them; otherwise one at the end does.
@@ -873,7 +896,8 @@ NormArgs norm_args(const BlockNorm& b, const Shape& s) {
   p.gate = b.gate; p.scale = b.scale; p.shift = b.shift; p.weight = b.weight; p.bias = b.bias;
   p.post_weight = b.post_weight;
   p.offsets = b.offsets;
-  p.N = b.p->N; p.D = b.p->D; p.G = b.p->G; p.pre = b.p->pre; p.post = b.p->post;
+  p.N = b.p->N; p.D = b.p->D; p.G = b.p->G; p.pre = b.p->pre & ~SVGEAR_NORM_CLEAR_REST; p.post = b.p->post;
+  p.clear = b.offsets && (b.p->pre & SVGEAR_NORM_CLEAR_REST);
   p.tpr = s.tpr; p.chunk = s.chunk; p.stages = s.stages; p.ring_bytes = s.ring_bytes;
   p.eps = b.p->eps; p.a = b.p->res_scale;
   p.r = b.r; p.h = b.h; p.dx = b.dx; p.dy = b.dy;

@@ -34,6 +34,7 @@ SVGEAR_BUDGET_GLOBAL = 1
 SVGEAR_NORM_NONE = 0
 SVGEAR_NORM_RMS = 1
 SVGEAR_NORM_LAYER = 2
+SVGEAR_NORM_CLEAR_REST = 16
 SVGEAR_PAIR_ADJACENT = 0
 SVGEAR_PAIR_HALF = 1
 SVGEAR_QKNORM_NONE = 0
@@ -516,13 +517,16 @@ def block_norm(x, y=None, *, gate=None, scale=None, shift=None, weight=None, bia
                res_scale: float = 1.0, offsets=None, dtype=None, want_h: bool = True, stream=None):
     """r = res_scale x + gate P(y) post_weight and h = (Q(r) weight + bias)(1 + scale) + shift through
     svgear_block_norm.  x [N, D], y [N, D] or None (r is x); gate, scale, shift [G, D] with the groups given
-    by offsets [G+1] or N/G rows each.  h has y's type, or `dtype` (default x's) without y.
+    by offsets [G+1] or N/G rows each.  h has y's type, or `dtype` (default x's) without y.  Rows from
+    offsets[G] on belong to no group and are zero in r and h (without y, r is x as it is).
     Returns (r, h); h is None with want_h=False."""
     import torch
     if y is not None and dtype is not None and dtype != y.dtype:
         raise ValueError(f"dtype {dtype} differs from y's {y.dtype}")
     dtype = y.dtype if y is not None else dtype or x.dtype
     p, ptrs = _norm_call(x, y, dtype, gate, scale, shift, weight, bias, post_weight, pre, post, eps, res_scale, offsets)
+    if offsets is not None:
+        p.pre |= SVGEAR_NORM_CLEAR_REST
     with _On(x.device, stream) as st:
         r = torch.empty_like(x) if y is not None else None
         h = torch.empty_like(x, dtype=dtype) if want_h else None
@@ -536,13 +540,16 @@ def block_norm_backward(x, y, dr, dh, *, gate=None, scale=None, shift=None, weig
                         eps: float = 1e-6, res_scale: float = 1.0, offsets=None, stream=None):
     """Gradients of block_norm for the gradients dr of r and dh of h (one may be None), through
     svgear_block_norm_backward.  The other arguments are the forward's.  Returns a dict with dx, dy, dgate,
-    dscale, dshift, dweight, dbias and dpost_weight; None for what the forward was not given."""
+    dscale, dshift, dweight, dbias and dpost_weight; None for what the forward was not given.  Rows from
+    offsets[G] on add to no sum and are zero in dx and dy (without y, where r is x, dx is dr there)."""
     import torch
     if dr is None and dh is None:
         raise ValueError("dr or dh expected")
     dtype = y.dtype if y is not None else dh.dtype if dh is not None else x.dtype
     p, ptrs = _norm_call(x, y, dtype, gate, scale, shift, weight, bias, post_weight, pre, post, eps, res_scale, offsets)
     px, py, pgate, pscale, _, pweight, pbias, ppost, poff = ptrs
+    if offsets is not None:
+        p.pre |= SVGEAR_NORM_CLEAR_REST
     pdr, pdh = _want("dr", dr, x.dtype, x.shape, x.device), _want("dh", dh, dtype, x.shape, x.device)
     with _On(x.device, stream) as st:
         given = {"dx": x, "dy": y, "dgate": gate, "dscale": scale, "dshift": shift, "dweight": weight, "dbias": bias,

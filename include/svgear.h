@@ -359,19 +359,22 @@ SVGEAR_API int svgear_forward(const void* Q, const void* K, const void* V, const
  *         stands for 1, 0, 0, 1, 0, 1.
  *   offsets [G+1] int32: group g is the rows [offsets[g], offsets[g+1]),
  *         ascending from 0, empty groups allowed; rows from offsets[G] on are
- *         left as they were.  NULL: G groups of N/G rows (N a multiple of G).
- *         Values outside [0, N] are clamped.
+ *         left as they were, or are written as zeros when
+ *         SVGEAR_NORM_CLEAR_REST is or-ed to p->pre (for outputs in fresh
+ *         memory).  NULL: G groups of N/G rows (N a multiple of G).  Values
+ *         outside [0, N] are clamped.
  *   y NULL: gate and post_weight NULL, post NONE, res_scale 1, r NULL.
  *   h NULL: only r is formed.
  * r may be x, and h may be y (or x when y is NULL) where the types agree.
  * D a multiple of 8, at most 8192, and N at most 2^30 (else
  * SVGEAR_ERR_UNSUPPORTED); eps > 0.
  * ------------------------------------------------------------------------- */
-typedef enum { SVGEAR_NORM_NONE = 0, SVGEAR_NORM_RMS = 1, SVGEAR_NORM_LAYER = 2 } svgear_norm;
+typedef enum { SVGEAR_NORM_NONE = 0, SVGEAR_NORM_RMS = 1, SVGEAR_NORM_LAYER = 2, SVGEAR_NORM_CLEAR_REST = 16 } svgear_norm;
 
 typedef struct {
   int N, D, G;     /* rows, columns, groups of rows */
-  int pre, post;   /* svgear_norm of r (before the next block) and of y (after this one) */
+  int pre, post;   /* svgear_norm of r (before the next block) and of y (after this one);
+                      pre may have SVGEAR_NORM_CLEAR_REST or-ed to it */
   float eps;       /* added to the mean square under the root */
   float res_scale; /* factor of x in r */
   int dtype;       /* svgear_dtype of y, h, dy, dh */
@@ -389,7 +392,9 @@ SVGEAR_API int svgear_block_norm(const void* x, const void* y, const float* gate
  *   dx [N,D] res_dtype, dy [N,D] dtype (NULL exactly when y is NULL),
  *   dgate, dscale, dshift [G,D], dweight, dbias, dpost_weight [D] float32,
  *   each NULL when not wanted (dgate and dpost_weight need y).
- * Rows from offsets[G] on are neither read into a sum nor written.  The sums
+ * Rows from offsets[G] on are neither read into a sum nor written; with
+ * SVGEAR_NORM_CLEAR_REST dx and dy are zeros there (dx is dr there when y is
+ * NULL, since r is x).  The sums
  * over rows are added in a fixed order (same bits on every call).
  * dx may be x or dr, dy may be y or dh.
  *   ws: svgear_block_norm_backward_workspace_size(p) bytes. */

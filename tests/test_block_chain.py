@@ -164,3 +164,22 @@ def test_gradients_of_the_trained_parts_chain():
     # two float32 passes of well-conditioned rows: relative 1e-5 of the sum of magnitudes is hundreds of roundings
     assert abs((got * v).sum() - want) <= 1e-5 * (got * v).abs().sum(), ((got * v).sum(), want)
     assert np.isfinite(float(want))
+
+
+def test_rows_behind_the_last_group_are_zero_rows(monkeypatch):
+    """Offsets that end before the last row, on memory that holds NaN: the block's rows of no group are zeros going
+    into the projection and in its outputs, so every other row is what the steps give for such an input."""
+    x, w, m = inputs(seed=4)
+    end = N - 100
+    off = torch.tensor([0, 300, end], dtype=torch.int32, device="cuda")
+    _, n = sv.block_norm(x, scale=m["scale"], shift=m["shift"], offsets=off)
+    n[end:] = 0
+    q, k, v = sv.mx_linear(n, *w.qkv, w.qkv_bias).view(N, 3, H, d).unbind(1)
+    Q, K, V = sv.qkv_rope(q, k, v, axes=AXES, grid=GRID, wq=w.q_norm, wk=w.k_norm, norm=sv.SVGEAR_QKNORM_TOKEN)
+    y = sv.mx_product(*sv.mx_quantize(sv.forward(Q, K, V, **CL)[0]), *w.out, w.out_bias)
+    r, h = sv.block_norm(x, y, gate=m["gate"], scale=m["next_scale"], shift=m["next_shift"], offsets=off)
+    real = torch.empty_like
+    monkeypatch.setattr(torch, "empty_like", lambda *a, **kw: real(*a, **kw).fill_(math.nan))
+    r2, h2 = attention_block(x, w, H, axes=AXES, grid=GRID, offsets=off, **CL, **m)
+    assert torch.equal(r[:end], r2[:end]) and torch.equal(h[:end], h2[:end]) and r2.isfinite().all()
+    assert (r2[end:] == 0).all() and (h2[end:] == 0).all()

@@ -470,3 +470,59 @@ def test_refusals_of_tensors():
         sv.block_norm(x, gate=torch.zeros(1, 64, device="cuda"))  # a gate without y
     with pytest.raises(ValueError, match="unsupported"):
         sv.block_norm(x.half())
+
+
+# ------------------------------------------- rows behind the last group
+
+def test_clear_rest_is_a_known_flag(L):
+    INV, flag = sv.SVGEAR_ERR_INVALID, sv.SVGEAR_NORM_CLEAR_REST
+    assert sv.svgear_block_norm_backward_workspace_size(P(pre=2 | flag)) == sv.svgear_block_norm_backward_workspace_size(P())
+    for kw in (dict(pre=3 | flag), dict(pre=flag << 1), dict(post=1 | flag)):
+        assert fwd(L, P(**kw)) == INV and bwd(L, P(**kw)) == INV, kw
+
+
+@pytest.fixture
+def poisoned(monkeypatch):
+    """New tensors hold NaN until something writes to them."""
+    real = torch.empty_like
+    monkeypatch.setattr(torch, "empty_like", lambda *a, **k: real(*a, **k).fill_(math.nan))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [24, 128, 256, 1024, 2560, 5120, 8192])
+@pytest.mark.parametrize("types", [(BF, BF), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("cuts", [[0, 10, 10, 41], [0, 0], [0, 599], [0, 600]])
+def test_helpers_clear_the_rows_behind_the_last_group(poisoned, D, types, cuts):
+    """The helpers' outputs are new memory, so the rows that no group owns have to be written too; the others are
+    those of a call without them."""
+    p = Problem(600, D, types=types, cuts=cuts, post="rms", seed=2)
+    kw, end = p.kw(), cuts[-1]
+    x, y, dr, dh = (t.cuda() for t in (p.x, p.y, p.dr, p.dh))
+    for t in (x, y, dr, dh):
+        t[end:] = math.nan  # padding: read into nothing
+    r, h = sv.block_norm(x, y, **kw)
+    got = sv.block_norm_backward(x, y, dr, dh, **kw)
+    for t in (r, h, got["dx"], got["dy"]):
+        assert (t[end:] == 0).all() and t[:end].isfinite().all()
+    assert all(got[n].isfinite().all() for n in got)
+    if end:
+        short = lambda t: t[:end].contiguous()  # noqa: E731
+        r2, h2 = sv.block_norm(short(x), short(y), **kw)
+        want = sv.block_norm_backward(short(x), short(y), short(dr), short(dh), **kw)
+        assert torch.equal(r[:end], r2) and torch.equal(h[:end], h2)
+        assert torch.equal(got["dx"][:end], want["dx"]) and torch.equal(got["dy"][:end], want["dy"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 2048])
+def test_without_a_branch_the_rows_behind_pass_through(poisoned, D):
+    """r is x itself, so the gradient of r is that of x where no group is."""
+    p = Problem(50, D, types=(F32, BF), cuts=[0, 7, 30], with_y=False, seed=4)
+    kw = p.kw()
+    x, dr, dh = p.x.cuda(), p.dr.cuda(), p.dh.cuda()
+    r, h = sv.block_norm(x, dtype=BF, **kw)
+    assert r is x and (h[30:] == 0).all() and h[:30].isfinite().all()
+    dx = sv.block_norm_backward(x, None, dr, dh, **kw)["dx"]
+    assert torch.equal(dx[30:], dr[30:])
+    dx = sv.block_norm_backward(x, None, None, dh, **kw)["dx"]
+    assert (dx[30:] == 0).all() and dx.isfinite().all()

@@ -405,7 +405,7 @@ struct Ring {
     for (int k = 0; k < OPS; ++k) any |= p.in[k] != nullptr;
     // A wait that gives up records it; the block goes on with what is there, so every thread still meets every barrier.
     if (any) tc::mbar_wait(full + slot, parity, abort_flag, p.status);
-    // threads without an element read the first ones: they add to no sum and store nothing
+    // threads without a head read the first one's elements: their sums are replaced by zeros, and they store nothing
     const uint8_t* at = shared_base() + slot * OPS * row + (pl.on ? pl.off : 0) * sizeof(T);
 #pragma unroll
     for (int k = 0; k < OPS; ++k) {
@@ -676,11 +676,14 @@ __global__ void __launch_bounds__(Class<CLS, true>::kMax, (Class<CLS, true>::kTh
     return;
   }
   // Per-head weights: add the heads of this worker, in a warp, then over its warps.
+  // A thread without a head has multiplied zero gradients by another's elements, which gave NaN where those are
+  // infinite.  (pl.on, kept over the loop for this, would spill; threads inside a warp loaded zeros.)
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 a = halves(dw[k].A[i]), b = halves(dw[k].B[i]);
+      if (CLS != 0 && (int)threadIdx.x / pl.lanes >= p.H) a = b = make_float2(0.f, 0.f);
       for (int s = pl.lanes; s < (p.tpt < 32 ? p.tpt : 32); s <<= 1) {
         a.x += __shfl_xor_sync(0xffffffffu, a.x, s);
         a.y += __shfl_xor_sync(0xffffffffu, a.y, s);

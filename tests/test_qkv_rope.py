@@ -433,3 +433,27 @@ def test_refusals_of_tensors():
         sv.qkv_rope(x[:, :, :32].contiguous(), None, None, axes=(8, 8, 8), grid=(1, 2, 2))
     with pytest.raises(ValueError, match="unsupported"):
         sv.qkv_rope(x.half(), None, None, **ax)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,heads", [(64, (1, 3, 9, 19, 33)), (128, (1, 3, 5, 9, 18, 51))])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_an_infinity_stays_in_its_column_of_the_weight_gradient(d, heads, dtype):
+    """A head with one infinite element has an infinite norm: its other elements normalise to zero and add nothing
+    to the weight's gradient, whatever the number of heads leaves idle in the last warp."""
+    axes = (16, 24, 24) if d == 64 else (44, 42, 42)
+    for H in heads:
+        g = torch.Generator(device="cuda").manual_seed(H)
+        q = torch.randn(40, H, d, generator=g, device="cuda").to(dtype)
+        dQ = torch.randn(H, 40, d, generator=g, device="cuda").to(dtype)
+        w = 1 + 0.1 * torch.randn(d, generator=g, device="cuda")
+        kw = dict(axes=axes, grid=(1, 5, 8), norm=NORM["head"], wq=w)
+        without = dQ.clone()
+        without[0, 7] = 0  # that head's gradient
+        want = sv.qkv_rope_backward(without, None, None, q, None, **kw)
+        q[7, 0, 0] = math.inf
+        got = sv.qkv_rope_backward(dQ, None, None, q, None, **kw)
+        assert torch.equal(got["dwq"][1:], want["dwq"][1:]) and got["dwq"][0].isnan(), H
+        rest = torch.ones(40, H, dtype=torch.bool, device="cuda")
+        rest[7, 0] = False
+        assert torch.equal(got["dq"][rest], want["dq"][rest]), H

@@ -69,13 +69,31 @@ int check_rope(const svgear_rope_params* p) {
   return SVGEAR_OK;
 }
 
-// Rows start on 16-byte boundaries and distinct tokens do not overlap.
+// Rows start on 16-byte boundaries, and neighbours on either axis do not overlap.
 bool row_strides_ok(const svgear_rope_params* p, int64_t ld, int64_t batch) {
   const int es = esize(p->dtype);
   const int64_t width = (int64_t)p->H * p->d;
   if (ld % (16 / es) || batch % (16 / es)) return false;
   if (p->N > 1 && ld < width) return false;
   return p->B == 1 || batch >= width;
+}
+
+// No two rows of an output overlap (row_strides_ok holds): either one axis lies
+// within a step of the other, or no multiple of one stride comes nearer than a
+// row to a multiple of the other, within the axes' lengths.
+bool rows_apart(const svgear_rope_params* p, int64_t ld, int64_t batch) {
+  typedef __int128 wide;  // the strides are the caller's, whatever they are
+  const wide width = (wide)p->H * p->d;
+  if (p->N == 1 || p->B == 1) return true;
+  if (batch >= (p->N - 1) * (wide)ld + width || ld >= (p->B - 1) * (wide)batch + width) return true;
+  const bool few = p->B <= p->N;
+  const wide s1 = few ? batch : ld, s2 = few ? ld : batch;
+  const int n1 = few ? p->B : p->N, n2 = few ? p->N : p->B;  // n1 <= 2^15
+  for (int i = 1; i < n1; ++i) {
+    const wide at = i * s1, j = at / s2;
+    if ((j < n2 && at - j * s2 < width) || (j + 1 < n2 && (j + 1) * s2 - at < width)) return false;
+  }
+  return true;
 }
 
 int check_rope_inputs(const void* const in[3], const float* wq, const float* wk, const int32_t* pos,
@@ -195,7 +213,7 @@ int svgear_qkv_rope_backward(const void* dQ, const void* dK, const void* dV, con
     if (normed && i < 2 && grad[i] && !in[i]) return SVGEAR_ERR_INVALID;
   }
   if ((dwq && (!normed || !dQ)) || (dwk && (!normed || !dK))) return SVGEAR_ERR_INVALID;
-  if (!row_strides_ok(p, p->grad_ld, p->grad_batch)) return SVGEAR_ERR_INVALID;
+  if (!row_strides_ok(p, p->grad_ld, p->grad_batch) || !rows_apart(p, p->grad_ld, p->grad_batch)) return SVGEAR_ERR_INVALID;
   if (!aligned16(dQ, dK, dV, dq, dk, dv, dwq, dwk)) return SVGEAR_ERR_INVALID;
   if ((dwq || dwk) && (!ws || !aligned16(ws) || ws_bytes < qkv_rope_back_ws_bytes(p))) return SVGEAR_ERR_WORKSPACE;
   return cuda_status(qkv_rope_back_run(grad, in, wq, wk, positions, p, out, dwq, dwk, ws, S(stream)));

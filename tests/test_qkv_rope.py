@@ -457,3 +457,37 @@ def test_an_infinity_stays_in_its_column_of_the_weight_gradient(d, heads, dtype)
         rest = torch.ones(40, H, dtype=torch.bool, device="cuda")
         rest[7, 0] = False
         assert torch.equal(got["dq"][rest], want["dq"][rest]), H
+
+
+def test_overlapping_gradient_rows_are_refused(L):
+    """Two tokens' rows of an output that share memory would be written in no order.  All strides of a small grid
+    against a list of the rows: a layout that is taken gets as far as the missing workspace."""
+    W = 64
+    taken = 0
+    for B in (1, 2, 3, 4):
+        for N in (1, 2, 3, 5):
+            for ld in range(W, 7 * W, W // 2):
+                for batch in range(W, 12 * W, W // 2):
+                    starts = sorted(b * batch + n * ld for b in range(B) for n in range(N))
+                    apart = all(y - x >= W for x, y in zip(starts, starts[1:]))
+                    p = P(B=B, N=N, H=1, d=W, grid=(1, 1, 1), grad_ld=ld, grad_batch=batch)
+                    assert bwd(L, p, ws=None) == (sv.SVGEAR_ERR_WORKSPACE if apart else sv.SVGEAR_ERR_INVALID), (B, N, ld, batch)
+                    taken += apart
+    assert taken > 1000
+    for ld, batch in ((2 ** 62, 2 ** 62), (2 ** 62, W), (W, 2 ** 62)):  # no overflow on the way
+        assert bwd(L, P(B=3, N=3, H=1, d=W, grid=(1, 1, 1), grad_ld=ld, grad_batch=batch), ws=None) == (
+            sv.SVGEAR_ERR_INVALID if ld == batch else sv.SVGEAR_ERR_WORKSPACE)
+
+
+@pytest.mark.gpu
+def test_interleaved_gradient_rows():
+    """Rows of two batch entries between one another, as strides that are neither nested way round allow."""
+    W, N = 64, 3
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dQ = torch.randn(2, N, W, generator=g, device="cuda").to(BF)
+    p = sv.rope_params(2, N, 1, W, (16, 24, 24), (1, 1, 3), grad_ld=2 * W, grad_batch=3 * W)
+    out = torch.full((9, W), 7.0, dtype=BF, device="cuda")  # rows 0, 2, 4 and 3, 5, 7
+    sv.svgear_qkv_rope_backward(dQ, None, None, None, None, None, None, None, p, out, None, None, None, None, None, 0)
+    want = sv.qkv_rope_backward(dQ, None, None, H=1, axes=(16, 24, 24), grid=(1, 1, 3))["dq"]
+    assert torch.equal(out[[0, 2, 4]], want[0, :, 0]) and torch.equal(out[[3, 5, 7]], want[1, :, 0])
+    assert (out[[1, 6, 8]] == 7).all()

@@ -443,6 +443,8 @@ class _On:
         if stream is not None:
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+            elif stream.device.index != self.device:  # entering it would make its device current
+                raise ValueError(f"stream: one of {device} expected, got one of {stream.device}")
             self.ctx = (self.ctx or []) + [torch.cuda.stream(stream)]
 
     def __enter__(self):

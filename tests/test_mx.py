@@ -358,3 +358,46 @@ def test_refusals_of_tensors():
         sv.mx_linear(torch.zeros(4, 128, device="cuda"), c, s)
     with pytest.raises(sv.SvgearError):
         sv.mx_product(c, s, c, s)  # four features: not a multiple of 8
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 300])
+def test_chained_launches_captured_behind_copies_and_joined_streams(M):
+    """The product and the dequantisation recorded behind a copy, behind a fill, behind two joined streams and first
+    in a graph of their own: whatever stands ahead of them has ended before they read."""
+    N, K = 264, 1024
+    x = torch.randn(M, K, device="cuda").bfloat16()
+    w, sw = (t.cuda() for t in weights(N, K, 3))
+    codes, scales = sv.mx_quantize(x)
+    want, vals = sv.mx_product(codes, scales, w, sw), sv.mx_dequantize(codes, scales)
+    a, s = torch.zeros_like(codes), torch.zeros_like(scales)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def behind_a_copy():
+        a.zero_()
+        a.copy_(codes)
+        s.copy_(scales)
+
+    def behind_a_join():
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            a.copy_(codes)
+        s.copy_(scales)
+        main.wait_stream(side)
+
+    for ahead in (behind_a_copy, behind_a_join, lambda: None):
+        for call, ref in ((lambda: sv.mx_product(a, s, w, sw), want), (lambda: sv.mx_dequantize(a, s), vals)):
+            a.copy_(codes)
+            s.copy_(scales)
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=main):
+                ahead()
+                out = call()
+            for _ in range(3):
+                out.zero_()
+                graph.replay()
+                torch.cuda.synchronize()
+                assert torch.equal(out, ref)
+            del graph
+    assert sv.svgear_get_status() == sv.SVGEAR_OK

@@ -245,9 +245,10 @@ struct Ring {
   volatile int* abort_flag;
   int slot;         // the stage of the current row,
   uint32_t parity;  // and the parity of its phase
+  int stop;         // a wait has given up
   // One thread: the copies of `row` into stage s.
   __device__ __forceinline__ void issue(int row, int s) {
-    if (row >= end) return;
+    if (row >= end || stop) return;
     tc::mbar_arrive_expect_tx(full + s, bx + (p.y ? by : 0u) + (OPS == 4 ? (p.dr ? bx : 0u) + (p.dh ? by : 0u) : 0u));
     const uint32_t dst = tc::smem_u32(buf) + s * stage;
     tc::bulk_g2s(dst, static_cast<const char*>(p.x) + (long long)row * bx, bx, full + s);
@@ -258,7 +259,7 @@ struct Ring {
     }
   }
   __device__ __forceinline__ Ring(const NormArgs& args, const Columns<V>& cols, int row, int last)
-      : p(args), first(row), end(last), slot(-1), parity(1) {
+      : p(args), first(row), end(last), slot(-1), parity(1), stop(0) {
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ uint64_t bars[kMaxStages];
     __shared__ int flag;
@@ -284,8 +285,11 @@ struct Ring {
       slot = 0;
       parity ^= 1;
     }
-    // A wait that gives up records it; the block goes on with what is there, so every thread still meets every barrier.
+    // A wait that gives up records it; the block goes on with what is there, so every thread still meets every
+    // barrier, and copies no more: the stage's last copy may not have ended.  Those in flight were issued before the
+    // wait began and have had its limit to end.
     tc::mbar_wait(full + slot, parity, abort_flag, p.status);
+    stop = *abort_flag;
   }
   template <int K>
   __device__ __forceinline__ void read(Vec (&f)[V]) const {

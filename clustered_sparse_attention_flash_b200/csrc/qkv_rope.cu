@@ -369,9 +369,10 @@ struct Ring {
   volatile int* abort_flag;
   int slot;
   uint32_t parity;
+  int stop;          // a wait has given up
   // One thread: the copies of token `ahead` into stage s.
   __device__ __forceinline__ void issue(int s) {
-    if (t >= pl.end) return;
+    if (t >= pl.end || stop) return;
     uint32_t bytes = 0;
 #pragma unroll
     for (int k = 0; k < OPS; ++k) bytes += p.in[k] ? row : 0u;
@@ -386,7 +387,7 @@ struct Ring {
     ahead.step(p.N);
   }
   __device__ __forceinline__ Ring(const RopeArgs& args, const Place<D>& place)
-      : p(args), pl(place), ahead(args, place.t), t(place.t), row(args.H * D * sizeof(T)), slot(0), parity(0) {
+      : p(args), pl(place), ahead(args, place.t), t(place.t), row(args.H * D * sizeof(T)), slot(0), parity(0), stop(0) {
     __shared__ uint64_t bars[kMaxStages];
     __shared__ int flag;
     full = bars;
@@ -403,7 +404,9 @@ struct Ring {
     bool any = false;
 #pragma unroll
     for (int k = 0; k < OPS; ++k) any |= p.in[k] != nullptr;
-    // A wait that gives up records it; the block goes on with what is there, so every thread still meets every barrier.
+    // A wait that gives up records it; the block goes on with what is there, so every thread still meets every
+    // barrier, and copies no more: the stage's last copy may not have ended.  Those in flight were issued before the
+    // wait began and have had its limit to end.
     if (any) tc::mbar_wait(full + slot, parity, abort_flag, p.status);
     // threads without a head read the first one's elements: their sums are replaced by zeros, and they store nothing
     const uint8_t* at = shared_base() + slot * OPS * row + (pl.on ? pl.off : 0) * sizeof(T);
@@ -417,6 +420,7 @@ struct Ring {
         zero_raw(r[k][1]);
       }
     }
+    stop = *abort_flag;  // read here, it costs nothing; in release() 2 to 11 %
   }
   // Behind a barrier that follows take(): the stage is free for a later token.
   __device__ __forceinline__ void release() {

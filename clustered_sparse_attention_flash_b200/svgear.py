@@ -627,6 +627,9 @@ def qkv_rope(q, k, v, *, axes, grid=None, positions=None, wq=None, wk=None, orig
     x = q if q is not None else k if k is not None else v
     if x is None:
         raise ValueError("one of q, k, v expected")
+    if out is not None and (len(out) != 3 or any((o is None) != (t is None) or (o is not None and o.dim() != 3)
+                                                 for o, t in zip(out, (q, k, v)))):
+        raise ValueError("out: [B*H, M, d] for each of q, k, v that is given, None for the others")
     if not x.is_cuda:
         raise ValueError("device tensor expected")
     dev, dtype, shape = x.device, x.dtype, x.shape

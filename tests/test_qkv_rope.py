@@ -491,3 +491,12 @@ def test_interleaved_gradient_rows():
     want = sv.qkv_rope_backward(dQ, None, None, H=1, axes=(16, 24, 24), grid=(1, 1, 3))["dq"]
     assert torch.equal(out[[0, 2, 4]], want[0, :, 0]) and torch.equal(out[[3, 5, 7]], want[1, :, 0])
     assert (out[[1, 6, 8]] == 7).all()
+
+
+def test_outputs_have_to_match_the_inputs():
+    x, o = torch.zeros(4, 2, 64), torch.zeros(2, 4, 64)
+    for out in ((None, None, None), (o,), (o, o, o), (None, o, None), (o, None, None, None), (o[0], None, None)):
+        with pytest.raises(ValueError, match="out:"):
+            sv.qkv_rope(x, None, None, axes=(16, 24, 24), grid=(1, 2, 2), out=out)
+    with pytest.raises(ValueError, match="device tensor"):
+        sv.qkv_rope(x, None, None, axes=(16, 24, 24), grid=(1, 2, 2), out=(o, None, None))

@@ -183,3 +183,31 @@ def test_rows_behind_the_last_group_are_zero_rows(monkeypatch):
     r2, h2 = attention_block(x, w, H, axes=AXES, grid=GRID, offsets=off, **CL, **m)
     assert torch.equal(r[:end], r2[:end]) and torch.equal(h[:end], h2[:end]) and r2.isfinite().all()
     assert (r2[end:] == 0).all() and (h2[end:] == 0).all()
+
+
+@pytest.mark.parametrize("cuts", [(0, 100, N), (0, 1, 1023, 1023, N)])
+def test_float32_stream_and_ragged_groups_step_by_step(cuts):
+    """Each step of a block with a float32 residual stream against its formula, and the block against the steps."""
+    x, w, _ = inputs(torch.float32, seed=6)
+    n_groups = len(cuts) - 1
+    g = torch.Generator(device="cuda").manual_seed(7)
+    m = {n: torch.randn(n_groups, D, generator=g, device="cuda") * 0.3
+         for n in ("shift", "scale", "gate", "next_shift", "next_scale")}
+    off = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+    count = torch.tensor([b - a for a, b in zip(cuts, cuts[1:])], device="cuda")
+    rows = lambda t: t.double().repeat_interleave(count, 0)  # noqa: E731
+    R = 1.01 * 2.0 ** -8  # one rounding to bfloat16, as above
+    _, n = sv.block_norm(x, scale=m["scale"], shift=m["shift"], offsets=off, dtype=BF)
+    near(n, layer_norm(x) * (1 + rows(m["scale"])) + rows(m["shift"]), R, "norm")
+    q, k, v = sv.mx_linear(n, *w.qkv, w.qkv_bias).view(N, 3, H, d).unbind(1)
+    Q, K, V = sv.qkv_rope(q, k, v, axes=AXES, grid=GRID, wq=w.q_norm, wk=w.k_norm, norm=sv.SVGEAR_QKNORM_TOKEN)
+    y = sv.mx_product(*sv.mx_quantize(sv.forward(Q, K, V, **CL)[0]), *w.out, w.out_bias)
+    r, h = sv.block_norm(x, y, gate=m["gate"], scale=m["next_scale"], shift=m["next_shift"], offsets=off)
+    added = rows(m["gate"]) * y.double()
+    want = x.double() + added
+    # r = x + (g y): the product and the sum are rounded to float32, each within 2^-24 of its value
+    assert r.dtype == torch.float32 and h.dtype == BF
+    assert ((r.double() - want).abs() <= 2.0 ** -24 * 1.001 * (added.abs() + want.abs())).all()
+    near(h, layer_norm(want) * (1 + rows(m["next_scale"])) + rows(m["next_shift"]), R, "next norm")
+    r2, h2 = attention_block(x, w, H, axes=AXES, grid=GRID, offsets=off, **CL, **m)
+    assert torch.equal(r, r2) and torch.equal(h, h2)

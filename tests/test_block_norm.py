@@ -526,3 +526,42 @@ def test_without_a_branch_the_rows_behind_pass_through(poisoned, D):
     assert torch.equal(dx[30:], dr[30:])
     dx = sv.block_norm_backward(x, None, None, dh, **kw)["dx"]
     assert (dx[30:] == 0).all() and dx.isfinite().all()
+
+
+# ----------------------------------------------------------- in-place forms
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [48, 256, 640, 2048, 5120, 8192])
+@pytest.mark.parametrize("types", [(BF, BF), (F32, BF), (F32, F32)])
+def test_backward_in_place(D, types):
+    """dx in the place of x or of dr, dy in that of y or of dh: the bits of a call with outputs of their own."""
+    p = Problem(333, D, types=types, cuts=[0, 5, 5, 300], post="rms", seed=D)
+    kw = p.kw()
+    want = sv.block_norm_backward(*(t.cuda() for t in (p.x, p.y, p.dr, p.dh)), **kw)
+    P_, _ = sv._norm_call(p.x.cuda(), p.y.cuda(), types[1], *(kw[n] for n in (
+        "gate", "scale", "shift", "weight", "bias", "post_weight", "pre", "post", "eps", "res_scale", "offsets")))
+    ws = sv.workspace(sv.svgear_block_norm_backward_workspace_size(P_))
+    par = [kw[n] for n in ("gate", "scale", "weight", "bias", "post_weight", "offsets")]
+    for over_x, over_y in ((True, True), (True, False), (False, True), (False, False)):
+        x, y, dr, dh = (t.cuda() for t in (p.x, p.y, p.dr, p.dh))
+        dx, dy = (x if over_x else dr), (y if over_y else dh)
+        sums = [torch.full_like(kw[n], math.nan) for n in ("gate", "scale", "shift", "weight", "bias", "post_weight")]
+        sv.svgear_block_norm_backward(x, y, dr, dh, *par, P_, dx, dy, *sums, ws, ws.numel())
+        assert torch.equal(dx[:300], want["dx"][:300]) and torch.equal(dy[:300], want["dy"][:300])
+        assert torch.equal(dx[300:], (p.x if over_x else p.dr).cuda()[300:])
+        assert torch.equal(dy[300:], (p.y if over_y else p.dh).cuda()[300:])
+        for t, n in zip(sums, ("dgate", "dscale", "dshift", "dweight", "dbias", "dpost_weight")):
+            assert torch.equal(t, want[n]), n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [48, 1032, 5120])
+@pytest.mark.parametrize("types", [(BF, BF), (F32, F32)])
+def test_forward_in_place_without_a_branch(D, types):
+    p = Problem(333, D, types=types, with_y=False, G=1, seed=D)
+    kw, x = p.kw(), p.x.cuda()
+    _, want = sv.block_norm(x, **kw)
+    P_, _ = sv._norm_call(x, None, types[1], *(kw[n] for n in (
+        "gate", "scale", "shift", "weight", "bias", "post_weight", "pre", "post", "eps", "res_scale", "offsets")))
+    sv.svgear_block_norm(x, None, None, kw["scale"], kw["shift"], kw["weight"], kw["bias"], None, None, P_, None, x)
+    assert torch.equal(x, want)

@@ -401,3 +401,52 @@ def test_chained_launches_captured_behind_copies_and_joined_streams(M):
                 assert torch.equal(out, ref)
             del graph
     assert sv.svgear_get_status() == sv.SVGEAR_OK
+
+
+def small_numbers(M, K, seed, device="cpu"):
+    """Random codes under scales 1/2, 1 and 2: every product of two such matrices is a multiple of 2^-4."""
+    g = torch.Generator(device=device).manual_seed(seed)
+    return (torch.randint(0, 256, (M, K // 2), generator=g, dtype=torch.uint8, device=device),
+            torch.randint(126, 129, (M, K // 32), generator=g, dtype=torch.uint8, device=device))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(1, 8, 32), (1, 2048, 16384), (2, 40, 16384), (16, 512, 8192), (40, 136, 16384), (64, 1024, 5120),
+                                   (128, 256, 8192), (300, 264, 8224), (500, 512, 16384), (2000, 1032, 4128), (3000, 2304, 1056)])
+def test_sums_are_kept_to_float32_and_rounded_once(M, N, K):
+    """The magnitudes add up to less than 2^24 units of 2^-4, so that float32 holds every partial sum exactly in any
+    order, and the one rounding left is that of the result."""
+    a, sa = small_numbers(M, K, 1)
+    w, sw = small_numbers(N, K, 2)
+    bias = torch.randint(-4000, 4000, (N,), generator=torch.Generator().manual_seed(3)).float() / 16
+    A, W = (values(unpacked(c), s).cuda() for c, s in ((a, sa), (w, sw)))
+    ref = A @ W.T
+    assert ((A.abs() @ W.abs().T).amax() + 250) * 16 < 2 ** 24
+    dev = [t.cuda() for t in (a, sa, w, sw)]
+    assert torch.equal(sv.mx_product(*dev).double(), ref.to(BF).double())
+    assert torch.equal(sv.mx_product(*dev, bias.cuda()).double(), (ref + bias.double().cuda()).to(BF).double())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads", [False, True])
+def test_quantise_more_than_2_to_the_31_elements(heads):
+    M, K = 2 ** 21 + 64, 1024
+    x = torch.empty((8, M, 128) if heads else (M, K), dtype=BF, device="cuda").normal_()
+    codes, scales = sv.mx_quantize(x)
+    y = sv.mx_dequantize(codes, scales)
+    for at in (slice(0, 64), slice(M - 64, M)):
+        part = x[:, at].contiguous() if heads else x[at]
+        c, s = sv.mx_quantize(part)
+        assert torch.equal(codes[at], c) and torch.equal(scales[at], s)
+        assert torch.equal(y[at], sv.mx_dequantize(c, s))
+
+
+@pytest.mark.gpu
+def test_product_of_more_than_2_to_the_31_elements():
+    M, N, K = 2 ** 21 + 64, 1032, 512
+    a, sa = small_numbers(M, K, 1, "cuda")
+    w, sw = small_numbers(N, K, 2, "cuda")
+    y = sv.mx_product(a, sa, w, sw)
+    assert sv.svgear_get_status() == sv.SVGEAR_OK
+    for at in (slice(0, 64), slice(M // 2, M // 2 + 64), slice(M - 64, M)):
+        assert torch.equal(y[at], sv.mx_product(a[at], sa[at], w, sw))

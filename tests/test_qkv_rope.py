@@ -500,3 +500,57 @@ def test_outputs_have_to_match_the_inputs():
             sv.qkv_rope(x, None, None, axes=(16, 24, 24), grid=(1, 2, 2), out=out)
     with pytest.raises(ValueError, match="device tensor"):
         sv.qkv_rope(x, None, None, axes=(16, 24, 24), grid=(1, 2, 2), out=(o, None, None))
+
+
+@pytest.mark.gpu
+def test_more_than_2_to_the_31_elements():
+    N, H, d = 2 ** 17 + 70, 128, 128
+    x = torch.empty(N, H, d, dtype=BF, device="cuda").normal_()
+    w = 1 + 0.1 * torch.randn(H * d, device="cuda")
+    kw = dict(axes=(44, 42, 42), norm=NORM["token"], wq=w)
+    Q = sv.qkv_rope(x, None, None, grid=(1, 1, N), **kw)[0]
+    back = sv.qkv_rope_backward(Q, None, None, x, None, grid=(1, 1, N), **kw)["dq"]
+    for a in (0, N // 2, N - 64):
+        pos = torch.zeros(64, 3, dtype=torch.int32, device="cuda")
+        pos[:, 2] = torch.arange(a, a + 64, device="cuda")
+        part = sv.qkv_rope(x[a:a + 64], None, None, positions=pos, **kw)[0]
+        assert torch.equal(Q[:, a:a + 64], part)
+        assert torch.equal(back[a:a + 64], sv.qkv_rope_backward(part, None, None, x[a:a + 64], None, positions=pos, **kw)["dq"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("norm", ["head", "token"])
+def test_gradients_of_every_head_count(d, dtype, norm):
+    """The gradients through the norms, with every number of heads, against 64 bits on the device; bounds as above."""
+    N, g = 450, torch.Generator(device="cuda").manual_seed(7)
+    axes, grid = ((16, 24, 24) if d == 64 else (44, 42, 42)), (2, 15, 15)
+    wide = torch.randn(N, 16384 // d, d, generator=g, device="cuda").to(dtype)
+    grads = torch.randn(16384 // d, N, d, generator=g, device="cuda").to(dtype)
+    weights = 1 + 0.3 * torch.randn(16384, generator=g, device="cuda")
+    t = torch.arange(N, device="cuda")
+    pos = torch.stack([t // 225, t // 15 % 15, t % 15], -1).double()
+    ang = torch.cat([pos[:, a:a + 1] * 10000.0 ** (-2.0 * torch.arange(s // 2, device="cuda").double() / s)
+                     for a, s in enumerate(axes)], -1)
+    back = torch.polar(torch.ones_like(ang), -ang)[:, None]
+    dims = (-1,) if norm == "head" else (-1, -2)
+    for H in range(1, 16384 // d + 1):
+        x, dQ = wide[:, :H].contiguous(), grads[:H].contiguous()
+        w = weights[:d if norm == "head" else H * d].contiguous()
+        got = sv.qkv_rope_backward(dQ, None, None, x, None, axes=axes, grid=grid, norm=NORM[norm], wq=w)
+        X, W, G = x.double(), w.double().view(-1, d), dQ.double().transpose(0, 1).contiguous()
+        dz = torch.view_as_real(torch.view_as_complex(G.view(N, H, d // 2, 2)) * back).flatten(-2)
+        mag = (dz[..., 0::2].abs() + dz[..., 1::2].abs()).repeat_interleave(2, -1)
+        inv = 1 / torch.sqrt((X * X).mean(dims, keepdim=True) + 1e-6)
+        n, u = X * inv, dz * W
+        dx = inv * (u - n * (u * n).mean(dims, keepdim=True))
+        mag_dx = inv * (mag * W.abs()).amax(dims, keepdim=True) * (2 + 2 * n.abs().amax(dims, keepdim=True) * n.abs())
+        dw, mag_dw = (dz * n).sum(0), (mag * n.abs()).sum(0)
+        if norm == "head":
+            dw, mag_dw = dw.sum(0), mag_dw.sum(0)
+        count = N * (H if norm == "head" else 1)
+        for name, have, ref, m, k, c in (("dq", got["dq"], dx, mag_dx, dtype, 0),
+                                         ("dwq", got["dwq"], dw.flatten(), mag_dw.flatten(), F32, count)):
+            over = (have.double() - ref).abs() - ((K + c) * U * (m + ref.abs()) + HALF[k] * ref.abs() + 1e-37)
+            assert over.max() <= 0, (name, H, float(over.max()))

@@ -20,11 +20,17 @@
 // (packed float32, two vectors per thread, statistics behind one barrier: 458
 // to about 220 per warp and row), spills (with the ring's shared memory there
 // is no L1 left to catch them) and reads so far ahead that the writes wait (see
-// kBlocksRing).  Measured on a B200 (share of a plain copy's 6,544 GB/s): 75,600
-// x 5,120 bf16, gated residual and layer norm, 525 us, 5.9 TB/s (0.90); float32
-// 40,000 x 2,048 0.93, 30,000 x 4,096 0.98; backward 32,768 x 2,048 bf16 149 us,
-// 5.4 TB/s (0.83), of which 13 us are the column sums; backward 32,768 x 5,120
-// 0.65, where ten warps per SM issue 700 instructions a row each.
+// kBlocksRing).  Measured on a B200 (share of a plain copy's 6,544 GB/s), gated
+// residual and layer norm, stream / branch types:
+//   forward   75,600 x 5,120 bf16 525 us (0.90), float32 / bf16 770 us (0.92);
+//             40,000 x 2,048 float32 215 us (0.93), float32 / bf16 157 us (0.96)
+//   backward  32,768 x 2,048 bf16 148 us (0.83), of which 13 us are the column
+//             sums, float32 / bf16 199 us (0.93), float32 258 us (0.95);
+//             32,768 x 5,120 bf16 480 us (0.64), float32 / bf16 556 us (0.83),
+//             float32 631 us (0.98)
+// The backward pass of wide bf16 rows is the one far from its bytes: float32 rows,
+// twice as long, take a third more.  An SM holds one block of ten warps there,
+// which issue 700 instructions a row each and all stop at the same barriers.
 #include <algorithm>
 #include <type_traits>
 

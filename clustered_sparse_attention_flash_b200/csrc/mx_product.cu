@@ -89,12 +89,16 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int pitch, int 
 // Two neighbouring SMs work on one tile of 256 features x TN tokens
 // (cta_group::2): each holds its own 128 features and half of the tokens, so
 // that at TN = 192 an SM reads 7 KB of codes per 64 elements of K where a tile of
-// its own would read 10 KB.  What bounds it is the shared-memory port, which each
-// code passes once from TMA and once to the MMA, and the power limit: 75,600 x
-// 15,360 x 5,120 of quantised normal data takes 2.53 ms at TN = 224, 4.7 PFLOP/s,
-// 0.73 of four times the measured bf16 burst rate; with zeros for data, which
-// take less power, 5.6 PFLOP/s.  (TN = 192: 2.72 ms and 5.0 PFLOP/s; one SM per
-// tile of 128 x 192: 3.47 ms.)  Beside two accumulators of 224 tokens tensor
+// its own would read 10 KB.  What bounds it is how fast an SM takes in codes, 66
+// to 68 bytes per ns at every width (a stage of 256 elements of K is 20, 24, 28
+// and 30 KB at TN = 64, 128, 192 and 224 and takes 300, 375, 435 and 461 ns), so
+// a wider tile gains by its fewer bytes per product; and, at the largest sizes,
+// the power limit.  No one unit is at its peak: tensor pipe 63 % busy, 48 bytes a
+// clock from the L2 at 1.61 GHz.  75,600 x 15,360 x 5,120 of quantised normal data
+// takes 2.53 ms at TN = 224 when the chip is cool, 4.7 PFLOP/s, 0.73 of four times
+// the measured bf16 burst rate, and 2.8 ms in a row (0.65); with zeros for data,
+// which take less power, 5.6 PFLOP/s.  (TN = 192: 2.72 ms; one SM per tile of
+// 128 x 192: 3.47 ms.)  Beside two accumulators of 224 tokens tensor
 // memory holds the scales of two stages, so that a stage's scales wait for the
 // MMAs two stages back; narrower tiles have a slot for each stage of the ring.
 // The launcher chooses by the rounds of tiles.  The even block issues the MMAs

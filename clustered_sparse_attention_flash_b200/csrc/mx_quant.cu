@@ -9,10 +9,13 @@
 // shows in everything computed from it.
 //
 // HBM-bound: x in, half a byte plus 1/32 byte per element out.  Measured on a
-// B200, 32,768 x 2,048 bf16: quantisation of rows 26.1 us, 6.5 TB/s (0.99 of a plain
-// copy), of head-major rows 27.0 us (0.96; 75,600 x 5,120 166 us, 0.90),
-// dequantisation 27.8 us (0.93).  With the maximum taken element by element in
-// float32 the issue slots bound it: 31.5 and 30.5 us.
+// B200 (share of a plain copy's 6,544 GB/s; above 1 where part of the output
+// is still in the L2 at the end): 75,600 x 5,120, quantisation of rows bf16 148 us
+// (1.01), float32 259 us (1.03), head-major bf16 168 us (0.89), float32 274 us
+// (0.98); dequantisation to bf16 147 us (1.02), to float32 356 us (0.75), whose
+// stores are 16 bytes of every 32 at a time.  32,768 x 2,048 bf16: rows 26.1 us,
+// head-major 27.0 us, dequantisation 27.8 us.  With the maximum taken element by
+// element in float32 the issue slots bound it: 31.5 and 30.5 us.
 #include <cuda_fp16.h>
 
 #include "chain.cuh"

@@ -15,11 +15,13 @@
 // [d/2 + 8j, d/2 + 8j + 8), so that both pairings find their partners in one
 // thread: adjacent pairs inside each vector, half-split pairs across the two.
 //
-// Measured on a B200 (share of a plain copy's 6,544 GB/s): 75,600 tokens of 40
-// heads of 128, bf16, norm over the token, 749 us, 6.2 TB/s (0.95); the same in
-// float32 0.86; backward of 32,768 tokens of 16 heads 186 us, 5.8 TB/s (0.88);
-// 262,144 tokens of one head of 64 0.55, where the sines of a token cost as
-// much as its one head.
+// Measured on a B200 behind other work (share of a plain copy's 6,544 GB/s), norm
+// over the token: 75,600 tokens of 40 heads of 128, bf16 747 us (0.95; 769 us each
+// in a hundred calls in a row), float32 1,521 us (0.93); backward of 32,768 tokens
+// of 16 heads bf16 184 us (0.89), float32 355 us (0.93), of 40 heads bf16 505 us
+// (0.81).  262,144 tokens of one head of 64 without a norm 55 us (0.56): the sines
+// of a token cost as much as its one head, and those of the axes that did not move
+// are computed again.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -427,7 +427,9 @@ def forward(Q, K, V, Cq: int, Ck: int, iters: int, rho: float, scale: float = 0.
 # and workspaces are allocated on the same stream, so the caching allocator
 # never hands their memory to work the kernels are not ordered with.  They
 # check every tensor themselves and call the library with plain pointers: on
-# small inputs the host's time is the call's time.
+# small inputs the host's time is the call's time.  They do not take part in
+# autograd: their results are detached, and a gradient is a call of its own
+# (block_norm_backward, qkv_rope_backward).
 
 
 class _On:

@@ -342,7 +342,8 @@ SVGEAR_API int svgear_forward(const void* Q, const void* K, const void* V, const
  * overlap of an output with an input is not allowed.  Make the first call of
  * each on a device outside stream capture (it looks up the status word and
  * sets kernel attributes).  Results are the same bits on every call.  No call
- * keeps anything for the next one; calls on different streams may overlap.
+ * keeps anything for the next one; calls on different streams may overlap,
+ * whether one host thread makes them or several.
  * ======================================================================== */
 
 /* ---------------------------------------------------------------------------
@@ -484,8 +485,10 @@ SVGEAR_API int svgear_qkv_rope_backward(const void* dQ, const void* dK, const vo
 SVGEAR_API int svgear_mx_quantize(const void* X, int dtype, int M, int K, int head_d, uint8_t* codes,
                       uint8_t* scales, void* stream);
 
-/* Y [M][K] (dtype): the values that codes and scales stand for (exact in
- * float32 and, for scale bytes above 1, in bfloat16). */
+/* Y [M][K] (dtype): the values that codes and scales stand for, exact in
+ * float32 and, for scale bytes above 1, in bfloat16; magnitudes of 2^128 and
+ * above, which take a given scale byte of 253 or 254 (svgear_mx_quantize makes
+ * none above 252), become infinities. */
 SVGEAR_API int svgear_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int M, int K, void* Y,
                       int dtype, void* stream);
 

@@ -190,6 +190,12 @@ def _check(fn: str, code: int) -> None:
         raise SvgearError(fn, code)
 
 
+def _fits(fn: str, *counts: int) -> None:
+    """Refuses counts that a C int does not hold: ctypes would cut them to 32 bits, and a call of fewer rows run."""
+    if max(counts) > 0x7fffffff:
+        raise SvgearError(fn, SVGEAR_ERR_UNSUPPORTED)
+
+
 def params(H, Nq, Nk, d, Cq, Ck, iters, rho, scale=0.0, dtype=SVGEAR_BF16,
            router=SVGEAR_ROUTE_ERROR, budget=SVGEAR_BUDGET_ROW) -> svgear_params:
     return svgear_params(H, Nq, Nk, d, Cq, Ck, iters, rho, scale, dtype, router, budget)
@@ -337,16 +343,19 @@ def svgear_qkv_rope_backward(dQ, dK, dV, q, k, wq, wk, positions, p, dq, dk, dv,
 
 
 def svgear_mx_quantize(X, dtype, M, K, head_d, codes, scales, stream=None):
+    _fits("svgear_mx_quantize", M, K, head_d)
     _check("svgear_mx_quantize", lib().svgear_mx_quantize(
         _ptr(X), dtype, M, K, head_d, _ptr(codes), _ptr(scales), _stream(stream)))
 
 
 def svgear_mx_dequantize(codes, scales, M, K, Y, dtype, stream=None):
+    _fits("svgear_mx_dequantize", M, K)
     _check("svgear_mx_dequantize", lib().svgear_mx_dequantize(
         _ptr(codes), _ptr(scales), M, K, _ptr(Y), dtype, _stream(stream)))
 
 
 def svgear_mx_product(a_codes, a_scales, w_codes, w_scales, bias, M, N, K, Y, stream=None):
+    _fits("svgear_mx_product", M, N, K)
     _check("svgear_mx_product", lib().svgear_mx_product(
         _ptr(a_codes), _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), _ptr(bias), M, N, K, _ptr(Y),
         _stream(stream)))
@@ -509,6 +518,7 @@ def _norm_call(x, y, dtype, gate, scale, shift, weight, bias, post_weight, pre, 
         G = scale.shape[0]
     elif shift is not None:
         G = shift.shape[0]
+    _fits("svgear_block_norm", N, D, G)
     p = svgear_norm_params(N, D, G, pre, post, eps, res_scale, _code(dtype), _code(x.dtype))
     return p, (x.data_ptr(), _want("y", y, dtype, (N, D), dev), _want("gate", gate, f32, (G, D), dev),
                _want("scale", scale, f32, (G, D), dev), _want("shift", shift, f32, (G, D), dev),
@@ -716,6 +726,7 @@ def _rows_of(x):
 
 def _quantize(x, M, K, head_d, st):
     import torch
+    _fits("svgear_mx_quantize", M, K, head_d)
     codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
     scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
     _check("svgear_mx_quantize", lib().svgear_mx_quantize(
@@ -726,6 +737,7 @@ def _quantize(x, M, K, head_d, st):
 def _product(pa, psa, M, w_codes, w_scales, bias, dev, st):
     import torch
     N, K, u8 = w_codes.shape[0], w_codes.shape[1] * 2, torch.uint8
+    _fits("svgear_mx_product", M, N, K)
     ptrs = (_want("w_codes", w_codes, u8, (N, K // 2), dev), _want("w_scales", w_scales, u8, (N, K // 32), dev),
             _want("bias", bias, torch.float32, (N,), dev))
     y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
@@ -750,6 +762,7 @@ def mx_dequantize(codes, scales, dtype=None, stream=None):
         raise ValueError(f"codes: [M, K/2] expected, got shape {tuple(codes.shape)}")
     M, K, dev = codes.shape[0], codes.shape[1] * 2, codes.device
     dtype = dtype or torch.bfloat16
+    _fits("svgear_mx_dequantize", M, K)
     pc, ps = _want("codes", codes, torch.uint8, (M, K // 2), dev), _want("scales", scales, torch.uint8, (M, K // 32), dev)
     with _On(dev, stream) as st:
         y = torch.empty((M, K), dtype=dtype, device=dev)

@@ -71,6 +71,36 @@ class Means:
                                       *(t.data_ptr() for t in self.out), self.ws.data_ptr(), self.ws.numel(), stream)
 
 
+class Product:
+    """svgear_mx_quantize and svgear_mx_product."""
+    def __init__(self, M, N, K):
+        g = torch.Generator(device="cuda").manual_seed(M)
+        self.x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+        self.w = sv.mx_quantize(torch.randn(N, K, generator=g, device="cuda"))
+        u8 = dict(dtype=torch.uint8, device="cuda")
+        self.out = [torch.zeros(M, K // 2, **u8), torch.zeros(M, K // 32, **u8), torch.zeros(M, N, dtype=BF, device="cuda")]
+        self.shape = (M, N, K)
+
+    def call(self, stream):
+        (M, N, K), (c, s, y) = self.shape, (t.data_ptr() for t in self.out)
+        code = sv.lib().svgear_mx_quantize(self.x.data_ptr(), sv.SVGEAR_BF16, M, K, 0, c, s, stream)
+        return code or sv.lib().svgear_mx_product(c, s, self.w[0].data_ptr(), self.w[1].data_ptr(), None, M, N, K, y, stream)
+
+
+class Attention:
+    """svgear_forward of two heads."""
+    def __init__(self, N, Ck, d):
+        g = torch.Generator(device="cuda").manual_seed(N)
+        self.qkv = [torch.randn(2, N, d, generator=g, device="cuda").bfloat16() for _ in range(3)]
+        self.p = sv.params(2, N, N, d, 8, Ck, 2, 0.3)
+        self.ws = sv.workspace(sv.svgear_workspace_size(self.p))
+        self.out = [torch.zeros(2, N, d, dtype=BF, device="cuda")]
+
+    def call(self, stream):
+        return sv.lib().svgear_forward(*(t.data_ptr() for t in self.qkv), ctypes.byref(self.p), None, None,
+                                       self.out[0].data_ptr(), self.ws.data_ptr(), self.ws.numel(), stream, None)
+
+
 # two sizes of one kernel that ask for different amounts of shared memory
 PAIRS = {
     "norm": (lambda: Norm(1200, 5120, False), lambda: Norm(1, 5120, False)),
@@ -78,6 +108,9 @@ PAIRS = {
     "norm backward": (lambda: Norm(600, 5120, True), lambda: Norm(600, 2560, True)),
     "rope": (lambda: Rope(600, 40, False), lambda: Rope(300, 20, False)),
     "rope backward": (lambda: Rope(600, 16, True), lambda: Rope(1, 9, True)),
+    "product, few tokens": (lambda: Product(5, 512, 2048), lambda: Product(40, 128, 8192)),
+    "product": (lambda: Product(300, 512, 512), lambda: Product(1000, 2048, 256)),
+    "attention": (lambda: Attention(1024, 64, 128), lambda: Attention(512, 16, 128)),
     "k-means": (lambda: Means(512, 500), lambda: Means(512, 16)),
 }
 
@@ -107,10 +140,11 @@ def test_two_threads_launch_one_kernel(pair):
     calls, alone = pair
     streams = [torch.cuda.Stream() for _ in calls]
     refused, start = [0, 0], threading.Barrier(2)
+    rounds = 400 if isinstance(calls[0], Attention) else 4000
 
     def work(i):
         start.wait()
-        for _ in range(4000):
+        for _ in range(rounds):
             refused[i] += calls[i].call(streams[i].cuda_stream) != sv.SVGEAR_OK
 
     threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]

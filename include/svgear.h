@@ -456,8 +456,8 @@ SVGEAR_API int svgear_qkv_rope(const void* q, const void* k, const void* v, cons
 
 /* Gradients of svgear_qkv_rope: dQ, dK, dV [B*H][out_tokens][d] give dq, dk,
  * dv (element [b][n][h][t] at b*grad_batch + n*grad_ld + h*d + t, no two rows
- * of one of them overlapping; each NULL with its gradient) and dwq, dwk (NULL when not wanted).  q and k, the
- * forward's inputs, are read only with a norm.
+ * of one of them overlapping; each NULL with its gradient) and dwq, dwk (NULL
+ * when not wanted).  q and k, the forward's inputs, are read only with a norm.
  *   ws: svgear_qkv_rope_backward_workspace_size(p) bytes (0 without a norm;
  *   not needed when dwq and dwk are NULL). */
 SVGEAR_API size_t svgear_qkv_rope_backward_workspace_size(const svgear_rope_params* p);
